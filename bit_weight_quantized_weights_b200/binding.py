@@ -42,8 +42,10 @@ EXPORTED = [
     "wq_residual", "wq_select_salient", "wq_w4a16_gemv_corrected", "wq_w4a16_gemv_salient",
     "wq_test_set_wait", "wq_mx_quantize", "wq_mx_decompose", "wq_mx_gemv", "wq_msd_gemm_nf4",
     "wq_msd_decode_attention", "wq_msd_decode_attention_workspace",
-    "wq_test_set_attention_split", "wq_kv_block_values",
+    "wq_test_set_attention_split", "wq_kv_block_values", "wq_kv_append", "wq_kv_read",
 ]
+
+_DTYPES = {torch.bfloat16: WQ_BF16, torch.float16: WQ_FP16, torch.float32: WQ_FP32}
 
 
 class WqError(RuntimeError):
@@ -89,6 +91,10 @@ def _load():
                                               ctypes.c_int),
         "wq_test_set_attention_split": ([I32], ctypes.c_int),
         "wq_kv_block_values": ([P, I64, I64, I32, P, P], ctypes.c_int),
+        "wq_kv_append": ([P, P, ctypes.c_int, I64, I64, I32, ctypes.POINTER(I64),
+                          ctypes.POINTER(I64), I64, P, P, I64, P, P, P, P, P, P, P], ctypes.c_int),
+        "wq_kv_read": ([P, P, P, P, P, P, I64, I64, I32, I64, P, P, I64, P, P, ctypes.c_int,
+                        ctypes.POINTER(I64), ctypes.POINTER(I64), P], ctypes.c_int),
         "wq_msd_gemm_noalloc": ([P, I64, I64, I64, I32, I32, P, P, P, P, P], ctypes.c_int),
         "wq_residual": ([ctypes.c_int, P, I64, I64, I32, P, P, P, P, P], ctypes.c_int),
         "wq_select_salient": ([P, I64, I64, I32, P, P], ctypes.c_int),
@@ -471,6 +477,99 @@ def kv_quantize_values(v, stream=None):
     blocked = wq_kv_block_values(qw, b * hkv, length, d, stream=stream)
     return (blocked.view(b, hkv, (length + 7) // 8, d), sc.view(b, hkv, length),
             zr.view(b, hkv, length))
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: tensors of another are refused."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != dev:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
+
+
+def _kv_cache(k_cache, v_cache):
+    """Check the two parts of an INT4 cache against each other: (B, Hkv, capacity, D)."""
+    kq, ks, kz = k_cache
+    vq, vs, vz = v_cache
+    for t, dt, name in ((kq, torch.int32, "k_codes"), (ks, torch.float16, "k_scales"),
+                        (kz, torch.float16, "k_zeros"), (vq, torch.int32, "v_codes"),
+                        (vs, torch.float16, "v_scales"), (vz, torch.float16, "v_zeros")):
+        _cuda(t, dt, name)
+    if kq.dim() != 4 or ks.dim() != 3 or vq.dim() != 4:
+        raise ValueError("KV cache tensors have 4 (codes) and 3 (scales, zeros) dimensions")
+    b, hkv, cap = ks.shape
+    d = 8 * kq.shape[3]
+    if kq.shape[:3] != ks.shape or kz.shape != ks.shape or vs.shape != ks.shape or \
+            vz.shape != ks.shape or tuple(vq.shape) != (b, hkv, (cap + 7) // 8, d):
+        raise ValueError("KV cache shapes do not match each other")
+    return b, hkv, cap, d
+
+
+def kv_cache_alloc(b, hkv, capacity, d=128, device="cuda"):
+    """An empty INT4 cache with room for `capacity` tokens a sequence: (k_cache,
+    v_cache), each (codes, scales, zeros) as kv_quantize_keys and
+    kv_quantize_values return them, zero-filled."""
+    def part(*codes):
+        return (torch.zeros(b, hkv, *codes, dtype=torch.int32, device=device),
+                torch.zeros(b, hkv, capacity, dtype=torch.float16, device=device),
+                torch.zeros(b, hkv, capacity, dtype=torch.float16, device=device))
+    return part(capacity, d // 8), part((capacity + 7) // 8, d)
+
+
+def _kv_rows(k, v, cache, starts, offsets):
+    """Check packed rows [T, Hkv, D] against a cache: (T, dtype, strides of k and v)."""
+    b, hkv, _, d = cache
+    if not (k.is_cuda and v.is_cuda):
+        raise ValueError("k and v must be CUDA tensors")
+    if k.dtype not in _DTYPES or v.dtype != k.dtype:
+        raise ValueError("k and v must both be bfloat16, float16 or float32")
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != hkv or k.shape[2] != d:
+        raise ValueError("k and v must be [T, %d, %d], got %s and %s"
+                         % (hkv, d, tuple(k.shape), tuple(v.shape)))
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("the last dimension of k and v must be contiguous")
+    _cuda(starts, torch.int32, "starts")
+    _cuda(offsets, torch.int32, "offsets")
+    if starts.shape != (b,) or offsets.shape != (b + 1,):
+        raise ValueError("starts must be int32 [%d] and offsets int32 [%d]" % (b, b + 1))
+    pair = ctypes.c_int64 * 2
+    return (k.shape[0], _DTYPES[k.dtype], pair(k.stride(0), k.stride(1)),
+            pair(v.stride(0), v.stride(1)))
+
+
+def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
+    """Quantize new tokens into an INT4 cache: rows k and v [T, Hkv, D] (bf16,
+    fp16 or fp32; any strides with a contiguous last dimension that keep rows
+    16-byte aligned), sequence b's being offsets[b] .. offsets[b + 1] - 1
+    (int32 [B + 1]), written from cache position starts[b] (int32 [B]) on.
+    k_cache and v_cache (kv_cache_alloc) are updated in place."""
+    b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache)
+    t, dt, ks, vs = _kv_rows(k, v, cache, starts, offsets)
+    _on_current_device(k, v, starts, offsets, *k_cache, *v_cache)
+    _check(lib.wq_kv_append(_ptr(k), _ptr(v), dt, t, hkv, d, ks, vs, b, _ptr(starts),
+                            _ptr(offsets), cap, *map(_ptr, k_cache), *map(_ptr, v_cache),
+                            _stream(stream)), "wq_kv_append")
+
+
+def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k_out=None,
+               v_out=None, stream=None):
+    """Rows of an INT4 cache read back: (k, v) [total, Hkv, D] of dtype bf16,
+    fp16 or fp32, token t of sequence b (offsets[b] <= t < offsets[b + 1]) from
+    cache position starts[b] + t - offsets[b]. Rows behind offsets[B] of a
+    given k_out and v_out stay as they were."""
+    b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache)
+    if k_out is None:
+        k_out = torch.empty(total, hkv, d, dtype=dtype, device=k_cache[0].device)
+    if v_out is None:
+        v_out = torch.empty(total, hkv, d, dtype=dtype, device=k_cache[0].device)
+    t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets)
+    if t != total:
+        raise ValueError("k_out and v_out must have %d rows" % total)
+    _on_current_device(k_out, v_out, starts, offsets, *k_cache, *v_cache)
+    _check(lib.wq_kv_read(*map(_ptr, k_cache), *map(_ptr, v_cache), b, hkv, d, cap, _ptr(starts),
+                          _ptr(offsets), t, _ptr(k_out), _ptr(v_out), dt, ks, vs,
+                          _stream(stream)), "wq_kv_read")
+    return k_out, v_out
 
 
 def attention_workspace(b, hq, hkv, length, d, n_components, device):

@@ -39,6 +39,12 @@ wq_status launch_msd_nf4(const void*, int64_t, int64_t, int64_t, int32_t, const 
 size_t kv_msd_workspace_bytes(int64_t B, int64_t Hq, int64_t L, int32_t C);
 wq_status launch_kv_block_values(const uint32_t*, int64_t, int64_t, int32_t, uint32_t*,
                                  cudaStream_t);
+wq_status launch_kv_append(const void*, const void*, wq_dtype, int64_t, int64_t, const int64_t*,
+                           const int64_t*, int64_t, const int32_t*, const int32_t*, int64_t,
+                           void* const*, cudaStream_t);
+wq_status launch_kv_read(void*, void*, wq_dtype, int64_t, int64_t, const int64_t*, const int64_t*,
+                         int64_t, const int32_t*, const int32_t*, int64_t, const void* const*,
+                         cudaStream_t);
 extern std::atomic<int> g_kv_chunks_per_cta;
 wq_status launch_kv_msd(const void*, int64_t, int64_t, int64_t, int64_t, int32_t, const void*,
                         const void*, const void*, const void*, const void*, const void*, void*,
@@ -124,6 +130,35 @@ wq_status check_attention_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t L, i
     return WQ_ERR_UNSUPPORTED;
   if (B > 65535 || Hkv > 65535 || L > INT32_MAX - 256 || B * Hq > INT32_MAX)
     return WQ_ERR_UNSUPPORTED;
+  return WQ_OK;
+}
+
+// Checks of the KV-cache append and read-back: WQ_OK, or the status to return.
+// `none` is set where there is nothing to do.
+wq_status check_kv_rows(const void* k, const void* v, wq_dtype dt, int64_t T, int64_t Hkv,
+                        int32_t D, const int64_t* k_strides, const int64_t* v_strides, int64_t B,
+                        const int32_t* starts, const int32_t* offsets, int64_t cap,
+                        std::initializer_list<const void*> cache, bool* none) {
+  *none = false;
+  if (T < 0 || Hkv <= 0 || D <= 0 || B < 0 || cap <= 0) return WQ_ERR_INVALID_ARG;
+  if (dt != WQ_BF16 && dt != WQ_FP16 && dt != WQ_FP32) return WQ_ERR_INVALID_ARG;
+  if (D != 128) return WQ_ERR_UNSUPPORTED;
+  *none = T == 0 || B == 0;
+  if (*none) return WQ_OK;
+  if (!k || !v || !k_strides || !v_strides || !starts || !offsets) return WQ_ERR_INVALID_ARG;
+  for (const void* c : cache)
+    if (!c) return WQ_ERR_INVALID_ARG;
+  const int64_t unit = dt == WQ_FP32 ? 4 : 8;  // elements in 16 bytes
+  for (int i = 0; i < 2; ++i) {
+    if (k_strides[i] < 0 || v_strides[i] < 0) return WQ_ERR_INVALID_ARG;
+    if (k_strides[i] % unit != 0 || v_strides[i] % unit != 0) return WQ_ERR_ALIGNMENT;
+  }
+  if (!all_aligned({k, v}) || !all_aligned(cache)) return WQ_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(offsets)) & 3u)
+    return WQ_ERR_ALIGNMENT;
+  if (T > INT32_MAX || cap > INT32_MAX - 7 || B > 65535 || Hkv > 65535)
+    return WQ_ERR_UNSUPPORTED;
+  if ((T / 8 + 2 * B) * Hkv > INT32_MAX - 8) return WQ_ERR_UNSUPPORTED;
   return WQ_OK;
 }
 
@@ -414,6 +449,38 @@ wq_status wq_kv_block_values(const uint32_t* codes, int64_t rows, int64_t L, int
   if (!all_aligned({codes, out})) return WQ_ERR_ALIGNMENT;
   if (L > INT32_MAX - 8 || D > 65536) return WQ_ERR_UNSUPPORTED;
   return guarded([&] { return launch_kv_block_values(codes, rows, L, D, out, as_stream(stream)); });
+}
+
+wq_status wq_kv_append(const void* k, const void* v, wq_dtype dtype, int64_t T, int64_t Hkv,
+                       int32_t D, const int64_t* k_strides, const int64_t* v_strides, int64_t B,
+                       const int32_t* starts, const int32_t* offsets, int64_t cap, void* k_codes,
+                       void* k_scales, void* k_zeros, void* v_codes, void* v_scales, void* v_zeros,
+                       void* stream) {
+  bool none;
+  wq_status s = check_kv_rows(k, v, dtype, T, Hkv, D, k_strides, v_strides, B, starts, offsets, cap,
+                              {k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros}, &none);
+  if (s != WQ_OK || none) return s;
+  void* const cache[6] = {k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros};
+  return guarded([&] {
+    return launch_kv_append(k, v, dtype, T, Hkv, k_strides, v_strides, B, starts, offsets, cap,
+                            cache, as_stream(stream));
+  });
+}
+
+wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_zeros,
+                     const void* v_codes, const void* v_scales, const void* v_zeros, int64_t B,
+                     int64_t Hkv, int32_t D, int64_t cap, const int32_t* starts,
+                     const int32_t* offsets, int64_t T, void* k, void* v, wq_dtype dtype,
+                     const int64_t* k_strides, const int64_t* v_strides, void* stream) {
+  bool none;
+  wq_status s = check_kv_rows(k, v, dtype, T, Hkv, D, k_strides, v_strides, B, starts, offsets, cap,
+                              {k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros}, &none);
+  if (s != WQ_OK || none) return s;
+  const void* const cache[6] = {k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros};
+  return guarded([&] {
+    return launch_kv_read(k, v, dtype, T, Hkv, k_strides, v_strides, B, starts, offsets, cap,
+                          cache, as_stream(stream));
+  });
 }
 
 wq_status wq_msd_decode_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t L,

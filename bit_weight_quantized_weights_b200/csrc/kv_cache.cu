@@ -1,0 +1,422 @@
+// Writing new tokens into an INT4 KV cache and reading rows of it back.
+//
+// The cache is the one wq_msd_decode_attention reads, with room for `cap`
+// tokens a sequence: one INT4 asymmetric group per (sequence, head, token) row,
+//   s = fp16(fp32(max(0, max x) - min(0, min x)) / 15)  ([-1, 1] if that is 0),
+//   z = clamp(rint(-min(0, min x) / s), 0, 15), q = clamp(rint(x / s) + z, 0, 15),
+// K codes a token a row (uint32 [B, Hkv, cap, 16]), V codes in blocks of 8
+// tokens (uint32 [B, Hkv, ceil(cap / 8), 128]: token t of dimension d in
+// nibble t % 8). A row read back is RN((q - z) s); (q - z) s is exact in fp32.
+//
+// Both kernels stream rows once and are bound by HBM: per row of 128 elements
+// the append reads 256 B (16-bit types) and writes 68 B, the read-back the
+// reverse. The unit of work is one V block, 8 cache positions of one
+// (sequence, head), taken by one warp: 16 lanes hold a row (8 elements a lane,
+// one 16-byte access), the two halves of the warp hold two rows, four steps
+// cover the block. So a V word has one writer (no atomics; the nibbles of
+// positions that are not written are read and put back), a K word is the 8
+// elements of one lane, and the group's minimum and maximum take 4 shuffles.
+// The warps of a CTA take neighbouring heads, whose rows lie side by side in
+// the packed [T, Hkv, D] tensors.
+//
+// Sequences are packed: offsets[b] .. offsets[b + 1] are sequence b's tokens,
+// starts[b] the cache position of the first. A sequence of n tokens touches
+// at most floor((n + 14) / 8) blocks, so giving it the unit numbers from
+// offsets[b] / 8 + 2 b on never overlaps the next one's, and a warp finds its
+// sequence by a 32-way search in `offsets` without any prefix sum. Every
+// position is checked against the capacity and every token against T on the
+// device, whatever the two arrays hold.
+#include "common.cuh"
+
+namespace wq {
+namespace {
+
+constexpr int kD = 128;
+
+struct KvRows {            // packed rows and where they belong
+  const int32_t* starts;   // [B]
+  const int32_t* offsets;  // [B + 1]
+  int64_t T;
+  int64_t cap;
+  int64_t units;           // T / 8 + 2 B
+  int64_t kts, khs, vts, vhs;  // token and head strides of the rows (elements)
+  int B, H;
+  int nblk;                // ceil(cap / 8)
+};
+
+// 32-way search: the last b in [0, B) whose first unit offsets[b] / 8 + 2 b is
+// at most u (0 if there is none).
+__device__ __forceinline__ int find_seq(const int32_t* offsets, int B, int64_t u, int lane) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int i = lane * step;
+    const bool in = i < n;
+    const int64_t first = in ? (int64_t)(offsets[lo + i] >> 3) + 2 * (int64_t)(lo + i) : 0;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, in && first <= u));
+    const int skip = (cnt > 0 ? cnt - 1 : 0) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
+// What a warp works on: block `blk` of sequence b and, for its lane's half,
+// the token index of each of its 4 rows (-1: not written or read).
+struct Unit {
+  int b;
+  int64_t blk;
+  int64_t tok[4];
+  bool any;
+};
+
+__device__ __forceinline__ Unit find_unit(const KvRows& p, int64_t u, int half, int lane,
+                                          bool clip) {
+  Unit w;
+  w.b = find_seq(p.offsets, p.B, u, lane);
+  const int64_t t0 = p.offsets[w.b], t1 = p.offsets[w.b + 1];
+  const int64_t first = p.starts[w.b];
+  const int64_t local = u - ((t0 >> 3) + 2 * (int64_t)w.b);
+  w.blk = (first >> 3) + local;
+  w.any = local >= 0 && 8 * w.blk < first + (t1 - t0);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t pos = 8 * w.blk + 2 * r + half;
+    const int64_t t = t0 + pos - first;
+    const bool ok = w.any && pos >= first && t < t1 && t >= 0 && t < p.T &&
+                    (!clip || (pos >= 0 && pos < p.cap));
+    w.tok[r] = ok ? t : -1;
+  }
+  return w;
+}
+
+template <typename T>
+struct Row;  // 8 consecutive elements of a row
+template <>
+struct Row<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = ld_stream_u4(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo_to_f32(w[i]);
+      f[2 * i + 1] = bf16_hi_to_f32(w[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+    st_stream_u4(p, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+  }
+};
+template <>
+struct Row<__half> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __half* p) { v = ld_stream_u4(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    }
+  }
+  static __device__ __forceinline__ void store(__half* p, const float (&f)[8]) {
+    st_stream_u4(p, make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]),
+                               pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7])));
+  }
+};
+template <>
+struct Row<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = ld_stream_u4(p);
+    b = ld_stream_u4(p + 4);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+    st_stream_u4(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]),
+                               __float_as_uint(f[2]), __float_as_uint(f[3])));
+    st_stream_u4(p + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]),
+                                   __float_as_uint(f[6]), __float_as_uint(f[7])));
+  }
+};
+
+// a / b rounded to nearest from y = RN(1 / b): one correction step on the
+// product a y (Markstein's theorem, with the residual a - b q exact in a fused
+// multiply-add). Where a quotient underflows the result is still below 1/2 in
+// magnitude, which is all its rounding to an integer needs.
+__device__ __forceinline__ float div_by(float a, float b, float y) {
+  const float q = a * y;
+  return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
+}
+
+// One group of 16 lanes x 8 elements: codes (0..15), scale and zero.
+__device__ __forceinline__ void quantize_row(const float (&f)[8], uint32_t (&c)[8], __half& sh,
+                                             int& z) {
+  float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo = fminf(lo, f[i]);
+    hi = fmaxf(hi, f[i]);
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+  if (__half2float(sh) == 0.0f) {  // an all-zero (or vanishing) row: range [-1, 1]
+    lo = -1.0f;
+    sh = __float2half_rn(__fdiv_rn(2.0f, 15.0f));
+  }
+  const float s = __half2float(sh);
+  const float y = __frcp_rn(s);
+  z = (int)fminf(fmaxf(rintf(div_by(-lo, s, y)), 0.0f), 15.0f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // rint(x / s) by adding 1.5 * 2^23 (|x / s| <= 30: fp16's smallest scales
+    // are off by at most half of themselves)
+    const float r = __fadd_rn(div_by(f[i], s, y), 12582912.0f);
+    const int q = (int)(__float_as_uint(r) - 0x4B400000u) + z;
+    c[i] = (uint32_t)min(max(q, 0), 15);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    kv_append_kernel(KvRows p, const T* __restrict__ k, const T* __restrict__ v,
+                     uint32_t* __restrict__ kc, __half* __restrict__ ks, __half* __restrict__ kz,
+                     uint32_t* __restrict__ vc, __half* __restrict__ vs,
+                     __half* __restrict__ vz) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
+  const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);  // units * H < 2^31 - 8
+  if (item >= (uint32_t)(p.units * p.H)) return;
+  const int h = (int)(item % (uint32_t)p.H);
+  const Unit w = find_unit(p, item / (uint32_t)p.H, half, lane, true);
+  if (!w.any) return;
+  // bit t: position 8 blk + t is written
+  const uint32_t mine = (w.tok[0] >= 0 ? 1u : 0u) | (w.tok[1] >= 0 ? 4u : 0u) |
+                        (w.tok[2] >= 0 ? 16u : 0u) | (w.tok[3] >= 0 ? 64u : 0u);
+  const uint32_t even = __shfl_sync(0xffffffffu, mine, 0);
+  const uint32_t odd = __shfl_sync(0xffffffffu, mine, 16);
+  const uint32_t mask = even | (odd << 1);
+  if (mask == 0) return;
+
+  Row<T> kr[4], vr[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (w.tok[r] >= 0) {
+      kr[r].load(k + w.tok[r] * p.kts + h * p.khs + 8 * col);
+      vr[r].load(v + w.tok[r] * p.vts + h * p.vhs + 8 * col);
+    } else {
+      kr[r].zero();
+      vr[r].zero();
+    }
+  }
+  const int64_t row0 = ((int64_t)w.b * p.H + h) * p.cap + 8 * w.blk;  // cache row of the block
+  uint4* vword = reinterpret_cast<uint4*>(
+      vc + (((int64_t)w.b * p.H + h) * p.nblk + w.blk) * kD + 8 * col + 4 * half);
+  uint4 old = make_uint4(0, 0, 0, 0);
+  if (mask != 0xFFu) old = *vword;
+
+  // rows r = 0..3 of this half are block positions 2 r + half
+  __half s_k = __float2half(0.0f), s_v = s_k, z_k = s_k, z_v = s_k;
+  uint32_t words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    // bits 2 r and 2 r + 1: either half has a row (the shuffles take both)
+    if (((mask >> (2 * r)) & 3u) == 0) continue;
+    float f[8];
+    uint32_t c[8];
+    __half s;
+    int z;
+    kr[r].get(f);
+    quantize_row(f, c, s, z);
+    if (w.tok[r] >= 0) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) word |= c[i] << (4 * i);
+      kc[(row0 + 2 * r + half) * (kD / 8) + col] = word;
+    }
+    if (col == r) {
+      s_k = s;
+      z_k = __int2half_rn(z);
+    }
+    vr[r].get(f);
+    quantize_row(f, c, s, z);
+    const int sh = 4 * (2 * r + half);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) words[i] |= c[i] << sh;
+    if (col == r) {
+      s_v = s;
+      z_v = __int2half_rn(z);
+    }
+  }
+  // lane col (< 4) holds row col's scales: one store an array covers the block
+  if (col < 4 && ((mask >> (2 * col + half)) & 1u)) {
+    const int64_t at = row0 + 2 * col + half;
+    ks[at] = s_k;
+    kz[at] = z_k;
+    vs[at] = s_v;
+    vz[at] = z_v;
+  }
+  // the two halves hold the even and the odd positions of the same 8 words:
+  // each keeps 4 of them
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t got =
+        __shfl_xor_sync(0xffffffffu, half ? words[j] : words[4 + j], 16);
+    o[j] = (half ? words[4 + j] : words[j]) | got;
+  }
+  if (mask != 0xFFu) {
+    // spread the 8 position bits to nibbles: keep the others' codes
+    uint32_t m = mask;
+    m = (m | (m << 12)) & 0x000F000Fu;
+    m = (m | (m << 6)) & 0x03030303u;
+    m = (m | (m << 3)) & 0x11111111u;
+    m *= 15u;
+    o[0] = (o[0] & m) | (old.x & ~m);
+    o[1] = (o[1] & m) | (old.y & ~m);
+    o[2] = (o[2] & m) | (old.z & ~m);
+    o[3] = (o[3] & m) | (old.w & ~m);
+  }
+  *vword = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// (q - z) s of 8 codes given in nibble `sh / 4` of 8 words, or in the 8
+// nibbles of one word: q as a float by placing it in the mantissa of 2^23.
+__device__ __forceinline__ float code_value(uint32_t w, int sh, float zb, float s) {
+  return (__uint_as_float(lop3_and_or(w >> sh, 15u, 0x4B000000u)) - zb) * s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    kv_read_kernel(KvRows p, const uint32_t* __restrict__ kc, const __half* __restrict__ ks,
+                   const __half* __restrict__ kz, const uint32_t* __restrict__ vc,
+                   const __half* __restrict__ vs, const __half* __restrict__ vz,
+                   T* __restrict__ k, T* __restrict__ v) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
+  const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);  // units * H < 2^31 - 8
+  if (item >= (uint32_t)(p.units * p.H)) return;
+  const int h = (int)(item % (uint32_t)p.H);
+  const Unit w = find_unit(p, item / (uint32_t)p.H, half, lane, false);
+  if (!w.any) return;
+  const int64_t row0 = ((int64_t)w.b * p.H + h) * p.cap + 8 * w.blk;
+  uint4 mine = make_uint4(0, 0, 0, 0);
+  if (w.blk >= 0 && w.blk < p.nblk)
+    mine = ld_stream_u4(vc + (((int64_t)w.b * p.H + h) * p.nblk + w.blk) * kD + 8 * col +
+                        4 * half);
+  uint32_t kw[4];
+  float sk[4], zk[4], sv[4], zv[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int64_t pos = 8 * w.blk + 2 * r + half;
+    const bool ok = w.tok[r] >= 0 && pos >= 0 && pos < p.cap;  // outside: rows of zeros
+    const int64_t at = row0 + 2 * r + half;
+    kw[r] = ok ? kc[at * (kD / 8) + col] : 0u;
+    sk[r] = ok ? __half2float(ks[at]) : 0.0f;
+    zk[r] = ok ? __half2float(kz[at]) + 8388608.0f : 8388608.0f;
+    sv[r] = ok ? __half2float(vs[at]) : 0.0f;
+    zv[r] = ok ? __half2float(vz[at]) + 8388608.0f : 8388608.0f;
+  }
+  // all 8 words of this lane's columns: 4 of its own, 4 of the other half's
+  const uint32_t own4[4] = {mine.x, mine.y, mine.z, mine.w};
+  uint32_t words[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, own4[j], 16);
+    words[j] = half ? got : own4[j];
+    words[4 + j] = half ? own4[j] : got;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (w.tok[r] < 0) continue;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = code_value(kw[r], 4 * i, zk[r], sk[r]);
+    Row<T>::store(k + w.tok[r] * p.kts + h * p.khs + 8 * col, f);
+    const int sh = 4 * (2 * r + half);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = code_value(words[i], sh, zv[r], sv[r]);
+    Row<T>::store(v + w.tok[r] * p.vts + h * p.vhs + 8 * col, f);
+  }
+}
+
+KvRows make_rows(int64_t T, int64_t Hkv, const int64_t* k_strides, const int64_t* v_strides,
+                 int64_t B, const int32_t* starts, const int32_t* offsets, int64_t cap) {
+  KvRows p;
+  p.starts = starts;
+  p.offsets = offsets;
+  p.T = T;
+  p.cap = cap;
+  p.units = T / 8 + 2 * B;
+  p.kts = k_strides[0];
+  p.khs = k_strides[1];
+  p.vts = v_strides[0];
+  p.vhs = v_strides[1];
+  p.B = (int)B;
+  p.H = (int)Hkv;
+  p.nblk = (int)((cap + 7) / 8);
+  return p;
+}
+
+template <typename T>
+void append(const KvRows& p, const void* k, const void* v, void* const* c, cudaStream_t st) {
+  const unsigned grid = (unsigned)((p.units * p.H + 7) / 8);
+  kv_append_kernel<T><<<grid, 256, 0, st>>>(
+      p, static_cast<const T*>(k), static_cast<const T*>(v), static_cast<uint32_t*>(c[0]),
+      static_cast<__half*>(c[1]), static_cast<__half*>(c[2]), static_cast<uint32_t*>(c[3]),
+      static_cast<__half*>(c[4]), static_cast<__half*>(c[5]));
+}
+
+template <typename T>
+void read_back(const KvRows& p, void* k, void* v, const void* const* c, cudaStream_t st) {
+  const unsigned grid = (unsigned)((p.units * p.H + 7) / 8);
+  kv_read_kernel<T><<<grid, 256, 0, st>>>(
+      p, static_cast<const uint32_t*>(c[0]), static_cast<const __half*>(c[1]),
+      static_cast<const __half*>(c[2]), static_cast<const uint32_t*>(c[3]),
+      static_cast<const __half*>(c[4]), static_cast<const __half*>(c[5]), static_cast<T*>(k),
+      static_cast<T*>(v));
+}
+
+}  // namespace
+
+wq_status launch_kv_append(const void* k, const void* v, wq_dtype dt, int64_t T, int64_t Hkv,
+                           const int64_t* k_strides, const int64_t* v_strides, int64_t B,
+                           const int32_t* starts, const int32_t* offsets, int64_t cap,
+                           void* const* cache, cudaStream_t st) {
+  const KvRows p = make_rows(T, Hkv, k_strides, v_strides, B, starts, offsets, cap);
+  if (dt == WQ_BF16)
+    append<__nv_bfloat16>(p, k, v, cache, st);
+  else if (dt == WQ_FP16)
+    append<__half>(p, k, v, cache, st);
+  else
+    append<float>(p, k, v, cache, st);
+  return launch_status();
+}
+
+wq_status launch_kv_read(void* k, void* v, wq_dtype dt, int64_t T, int64_t Hkv,
+                         const int64_t* k_strides, const int64_t* v_strides, int64_t B,
+                         const int32_t* starts, const int32_t* offsets, int64_t cap,
+                         const void* const* cache, cudaStream_t st) {
+  const KvRows p = make_rows(T, Hkv, k_strides, v_strides, B, starts, offsets, cap);
+  if (dt == WQ_BF16)
+    read_back<__nv_bfloat16>(p, k, v, cache, st);
+  else if (dt == WQ_FP16)
+    read_back<__half>(p, k, v, cache, st);
+  else
+    read_back<float>(p, k, v, cache, st);
+  return launch_status();
+}
+
+}  // namespace wq

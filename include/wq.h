@@ -427,6 +427,47 @@ wq_status wq_kv_block_values(const uint32_t* codes, int64_t rows, int64_t L, int
                              uint32_t* out, void* stream);
 
 /*
+ * New tokens into an INT4 KV cache with room for `cap` tokens a sequence, and
+ * rows of it read back. The cache is the one described at
+ * wq_msd_decode_attention, with L = cap: K codes uint32 [B, Hkv, cap, D/8], V
+ * codes uint32 [B, Hkv, ceil(cap/8), D], scales and zeros fp16 [B, Hkv, cap].
+ *   k, v     rows of T packed tokens, bf16, fp16 or fp32: element (t, h, d) at
+ *            t * strides[0] + h * strides[1] + d (strides in elements, host
+ *            arrays; each a non-negative multiple of 16 bytes), so that slices
+ *            of one fused projection's output and either head order are taken
+ *            as they are;
+ *   offsets  int32 [B + 1] (device): sequence b's tokens are t = offsets[b] ..
+ *            offsets[b + 1] - 1; non-decreasing, offsets[0] = 0, offsets[B]
+ *            <= T. Tokens behind offsets[B] are not read (append), rows behind
+ *            it not written (read);
+ *   starts   int32 [B] (device): token t of sequence b is at cache position
+ *            starts[b] + t - offsets[b].
+ * wq_kv_append quantizes every row as wq_quantize_pack(WQ_FMT_INT4_ASYM, group
+ * = D) does its fp32 value, bit for bit, and writes codes, scale and zero.
+ * Positions outside 0 .. cap - 1 are not written; all other rows of the cache
+ * stay as they were, also those that share a word of V codes with a new one.
+ * wq_kv_read writes RN_dtype((q - z) s) of every row (the product is exact in
+ * fp32), and rows of zeros for positions outside the cache.
+ * `starts` and `offsets` need 4-byte alignment, everything else 16. T == 0 and
+ * B == 0 are no-ops. D != 128, T > 2^31 - 1, cap > 2^31 - 8, B > 65535 or
+ * (T / 8 + 2 B) * Hkv > 2^31 - 9 return WQ_ERR_UNSUPPORTED. Non-finite rows
+ * give unspecified codes. Rows that repeat a cache position through
+ * overlapping sequences do not exist (every sequence has its own cache rows);
+ * offsets that decrease give unspecified rows, inside the buffers.
+ * Asynchronous on `stream`; every buffer is caller-owned.
+ */
+wq_status wq_kv_append(const void* k, const void* v, wq_dtype dtype, int64_t T, int64_t Hkv,
+                       int32_t D, const int64_t* k_strides, const int64_t* v_strides, int64_t B,
+                       const int32_t* starts, const int32_t* offsets, int64_t cap, void* k_codes,
+                       void* k_scales, void* k_zeros, void* v_codes, void* v_scales, void* v_zeros,
+                       void* stream);
+wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_zeros,
+                     const void* v_codes, const void* v_scales, const void* v_zeros, int64_t B,
+                     int64_t Hkv, int32_t D, int64_t cap, const int32_t* starts,
+                     const int32_t* offsets, int64_t T, void* k, void* v, wq_dtype dtype,
+                     const int64_t* k_strides, const int64_t* v_strides, void* stream);
+
+/*
  * Workspace bytes of wq_msd_decode_attention (0 for B == 0); the same shape
  * checks and status codes. Host only; `bytes` is a host pointer.
  */
