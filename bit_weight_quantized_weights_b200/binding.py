@@ -43,6 +43,7 @@ EXPORTED = [
     "wq_test_set_wait", "wq_mx_quantize", "wq_mx_decompose", "wq_mx_gemv", "wq_msd_gemm_nf4",
     "wq_msd_decode_attention", "wq_msd_decode_attention_workspace",
     "wq_test_set_attention_split", "wq_kv_block_values", "wq_kv_append", "wq_kv_read",
+    "wq_prefix_attention", "wq_prefix_attention_workspace",
 ]
 
 _DTYPES = {torch.bfloat16: WQ_BF16, torch.float16: WQ_FP16, torch.float32: WQ_FP32}
@@ -95,6 +96,10 @@ def _load():
                           ctypes.POINTER(I64), I64, P, P, I64, P, P, P, P, P, P, P], ctypes.c_int),
         "wq_kv_read": ([P, P, P, P, P, P, I64, I64, I32, I64, P, P, I64, P, P, ctypes.c_int,
                         ctypes.POINTER(I64), ctypes.POINTER(I64), P], ctypes.c_int),
+        "wq_prefix_attention": ([P, ctypes.c_int, I64, I64, I64, I64, I32, I64, I64, P, P, P, P, P,
+                                 P, I64, P, P, P, P, P, P, P, P, P, SZ, P], ctypes.c_int),
+        "wq_prefix_attention_workspace": ([I64, I64, I64, I32, I64, I64, ctypes.POINTER(SZ)],
+                                          ctypes.c_int),
         "wq_msd_gemm_noalloc": ([P, I64, I64, I64, I32, I32, P, P, P, P, P], ctypes.c_int),
         "wq_residual": ([ctypes.c_int, P, I64, I64, I32, P, P, P, P, P], ctypes.c_int),
         "wq_select_salient": ([P, I64, I64, I32, P, P], ctypes.c_int),
@@ -570,6 +575,60 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
                           _ptr(offsets), t, _ptr(k_out), _ptr(v_out), dt, ks, vs,
                           _stream(stream)), "wq_kv_read")
     return k_out, v_out
+
+
+def prefix_attention_workspace(b, hq, hkv, prefix_len, capacity, d=128, device="cuda"):
+    size = ctypes.c_size_t(0)
+    _check(lib.wq_prefix_attention_workspace(b, hq, hkv, d, prefix_len, capacity,
+                                             ctypes.byref(size)),
+           "wq_prefix_attention_workspace")
+    return torch.empty(max(int(size.value), 1), dtype=torch.uint8, device=device)
+
+
+def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix_len=None,
+                        workspace=None, out=None, stream=None):
+    """Decode attention over INT4 caches of a batch that shares a prefix: q
+    bf16 or fp16 [B, Hq, D] (contiguous heads, any stride between sequences);
+    prefix_k and prefix_v a cache of one sequence ([1, Hkv, ...]), of which the
+    first prefix_len tokens (default: all) are attended by every sequence;
+    k_cache and v_cache a cache of B sequences, of which sequence b attends the
+    first lengths[b] (int32 [B]) tokens. Returns out [B, Hq, D] of q's type.
+    prefix_k = prefix_v = None: no prefix."""
+    if not q.is_cuda or q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be a bfloat16 or float16 CUDA tensor")
+    b, hkv, cap, d = _kv_cache(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[0] != b or q.shape[2] != d:
+        raise ValueError("q must be [%d, Hq, %d], got %s" % (b, d, tuple(q.shape)))
+    hq = q.shape[1]
+    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+        raise ValueError("the heads of q must be contiguous")
+    _cuda(lengths, torch.int32, "lengths")
+    if lengths.shape != (b,):
+        raise ValueError("lengths must be int32 [%d]" % b)
+    if prefix_k is None and prefix_v is None:
+        prefix_k = prefix_v = (None, None, None)
+        pcap, prefix_len = 0, 0
+    else:
+        one, ph, pcap, pd = _kv_cache(prefix_k, prefix_v)
+        if (one, ph, pd) != (1, hkv, d):
+            raise ValueError("the prefix cache must be [1, %d, capacity, ...] with D = %d" % (hkv, d))
+        _on_current_device(*prefix_k, *prefix_v)
+        prefix_len = pcap if prefix_len is None else prefix_len
+    if workspace is None:
+        workspace = prefix_attention_workspace(b, hq, hkv, prefix_len, cap, d, q.device)
+    if out is None:
+        out = torch.empty(b, hq, d, dtype=q.dtype, device=q.device)
+    _cuda(out, q.dtype, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _on_current_device(q, lengths, workspace, out, *k_cache, *v_cache)
+    _check(lib.wq_prefix_attention(_ptr(q), _DTYPES[q.dtype], q.stride(0), b, hq, hkv, d,
+                                   prefix_len, pcap, *map(_ptr, prefix_k), *map(_ptr, prefix_v),
+                                   cap, *map(_ptr, k_cache), *map(_ptr, v_cache), _ptr(lengths),
+                                   _ptr(out), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)),
+           "wq_prefix_attention")
+    return out
 
 
 def attention_workspace(b, hq, hkv, length, d, n_components, device):

@@ -45,6 +45,10 @@ wq_status launch_kv_append(const void*, const void*, wq_dtype, int64_t, int64_t,
 wq_status launch_kv_read(void*, void*, wq_dtype, int64_t, int64_t, const int64_t*, const int64_t*,
                          int64_t, const int32_t*, const int32_t*, int64_t, const void* const*,
                          cudaStream_t);
+size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap);
+wq_status launch_prefix_attn(const void*, wq_dtype, int64_t, int64_t, int64_t, int64_t, int64_t,
+                             int64_t, const void* const*, int64_t, const void* const*,
+                             const int32_t*, void*, void*, cudaStream_t);
 extern std::atomic<int> g_kv_chunks_per_cta;
 wq_status launch_kv_msd(const void*, int64_t, int64_t, int64_t, int64_t, int32_t, const void*,
                         const void*, const void*, const void*, const void*, const void*, void*,
@@ -159,6 +163,17 @@ wq_status check_kv_rows(const void* k, const void* v, wq_dtype dt, int64_t T, in
   if (T > INT32_MAX || cap > INT32_MAX - 7 || B > 65535 || Hkv > 65535)
     return WQ_ERR_UNSUPPORTED;
   if ((T / 8 + 2 * B) * Hkv > INT32_MAX - 8) return WQ_ERR_UNSUPPORTED;
+  return WQ_OK;
+}
+
+// Shape checks of the shared-prefix attention: WQ_OK, or the status to return.
+wq_status check_prefix_shape(int64_t B, int64_t Hq, int64_t Hkv, int32_t D, int64_t P,
+                             int64_t cap) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || P < 0 || cap <= 0 || Hq % Hkv != 0)
+    return WQ_ERR_INVALID_ARG;
+  if (D != 128 || Hq / Hkv > 16) return WQ_ERR_UNSUPPORTED;
+  if (P > INT32_MAX - 7 || cap > INT32_MAX - 7) return WQ_ERR_UNSUPPORTED;
+  if (B > (1 << 30) || Hq > (1 << 30) || B * Hq > (1 << 30)) return WQ_ERR_UNSUPPORTED;
   return WQ_OK;
 }
 
@@ -480,6 +495,49 @@ wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_ze
   return guarded([&] {
     return launch_kv_read(k, v, dtype, T, Hkv, k_strides, v_strides, B, starts, offsets, cap,
                           cache, as_stream(stream));
+  });
+}
+
+wq_status wq_prefix_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int32_t D, int64_t P,
+                                        int64_t cap, size_t* bytes) {
+  if (!bytes) return WQ_ERR_INVALID_ARG;
+  wq_status s = check_prefix_shape(B, Hq, Hkv, D, P, cap);
+  if (s != WQ_OK) return s;
+  *bytes = B == 0 ? 0 : prefix_attn_workspace_bytes(B, Hq, Hkv, P, cap);
+  return WQ_OK;
+}
+
+wq_status wq_prefix_attention(const void* q, wq_dtype dtype, int64_t q_stride, int64_t B,
+                              int64_t Hq, int64_t Hkv, int32_t D, int64_t P, int64_t prefix_cap,
+                              const void* prefix_k_codes, const void* prefix_k_scales,
+                              const void* prefix_k_zeros, const void* prefix_v_codes,
+                              const void* prefix_v_scales, const void* prefix_v_zeros, int64_t cap,
+                              const void* k_codes, const void* k_scales, const void* k_zeros,
+                              const void* v_codes, const void* v_scales, const void* v_zeros,
+                              const int32_t* lengths, void* out, void* workspace, size_t ws_bytes,
+                              void* stream) {
+  wq_status s = check_prefix_shape(B, Hq, Hkv, D, P, cap);
+  if (s != WQ_OK) return s;
+  if ((dtype != WQ_BF16 && dtype != WQ_FP16) || q_stride < 0 || P > prefix_cap)
+    return WQ_ERR_INVALID_ARG;
+  if (prefix_cap > INT32_MAX - 7) return WQ_ERR_UNSUPPORTED;
+  if (B == 0) return WQ_OK;
+  const void* const pre[6] = {prefix_k_codes, prefix_k_scales, prefix_k_zeros,
+                              prefix_v_codes, prefix_v_scales, prefix_v_zeros};
+  const void* const own[6] = {k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros};
+  if (!q || !lengths || !out) return WQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 6; ++i) {
+    if (!own[i] || (P > 0 && !pre[i])) return WQ_ERR_INVALID_ARG;
+    if (!aligned16(own[i]) || !aligned16(pre[i])) return WQ_ERR_ALIGNMENT;
+  }
+  if (!all_aligned({q, out}) || q_stride % 8 != 0) return WQ_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(lengths) & 3u) return WQ_ERR_ALIGNMENT;
+  if (!workspace || ws_bytes < prefix_attn_workspace_bytes(B, Hq, Hkv, P, cap))
+    return WQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGNMENT;
+  return guarded([&] {
+    return launch_prefix_attn(q, dtype, q_stride, B, Hq, Hkv, P, prefix_cap, pre, cap, own,
+                              lengths, out, workspace, as_stream(stream));
   });
 }
 

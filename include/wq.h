@@ -468,6 +468,52 @@ wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_ze
                      const int64_t* k_strides, const int64_t* v_strides, void* stream);
 
 /*
+ * Decode attention of a batch whose sequences share a cached prefix ("shared
+ * prefix": one prompt, many answers), over INT4 caches. One new query token a
+ * sequence:
+ *   out[b, h] = softmax over the P prefix tokens and sequence b's own first
+ *               lengths[b] tokens of (q[b, h] . k / sqrt(D)) . v
+ * The prefix is read and multiplied once for all sequences of the batch.
+ *   q        bf16 or fp16 (`dtype`): head h of sequence b at b * q_stride +
+ *            h * D (elements; a multiple of 8), so that a slice of a fused
+ *            projection's output is taken as it is; Hq = R * Hkv, query head h
+ *            reads KV head h / R, 1 <= R <= 16; D == 128;
+ *   prefix   a cache of one sequence with room for prefix_cap tokens, the
+ *            first P of them the prefix (0 <= P <= prefix_cap);
+ *   own      a cache of B sequences with room for cap tokens each, in the
+ *            layout of wq_kv_append; lengths int32 [B] (device, 4-byte
+ *            aligned) counts the tokens held, clamped to 0 .. cap;
+ *   out      [B, Hq, D] of q's type. A sequence without any token (P == 0 and
+ *            length 0) gets zeros.
+ * Tokens behind P and behind a sequence's length are not read, whatever the
+ * buffers hold there. The codes enter fp16 tensor-core products as exact
+ * integers and scores, softmax statistics and sums are fp32; the softmax
+ * weights are rounded to fp16. Scales are those a quantizer writes (positive
+ * and finite). The result of a sequence does not depend on the values of
+ * other sequences. B == 0 is a no-op. With P == 0 the six prefix pointers may
+ * be NULL. prefix_cap or cap > 2^31 - 8, R > 16, B * Hq or B * R > 2^30 return
+ * WQ_ERR_UNSUPPORTED. Workspace: at least wq_prefix_attention_workspace(...)
+ * bytes for the same sizes; contents on entry do not matter, and calls that
+ * may overlap on the GPU need one each. Asynchronous on `stream`.
+ */
+wq_status wq_prefix_attention(const void* q, wq_dtype dtype, int64_t q_stride, int64_t B,
+                              int64_t Hq, int64_t Hkv, int32_t D, int64_t P, int64_t prefix_cap,
+                              const void* prefix_k_codes, const void* prefix_k_scales,
+                              const void* prefix_k_zeros, const void* prefix_v_codes,
+                              const void* prefix_v_scales, const void* prefix_v_zeros, int64_t cap,
+                              const void* k_codes, const void* k_scales, const void* k_zeros,
+                              const void* v_codes, const void* v_scales, const void* v_zeros,
+                              const int32_t* lengths, void* out, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Workspace bytes of wq_prefix_attention (0 for B == 0); the same shape checks
+ * and status codes. Host only; `bytes` is a host pointer.
+ */
+wq_status wq_prefix_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, int32_t D, int64_t P,
+                                        int64_t cap, size_t* bytes);
+
+/*
  * Workspace bytes of wq_msd_decode_attention (0 for B == 0); the same shape
  * checks and status codes. Host only; `bytes` is a host pointer.
  */

@@ -59,3 +59,29 @@ def value_words(codes):
     for t in range(8):
         out |= full[:, :, t::8] << np.uint32(4 * t)
     return out
+
+
+def prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix_len):
+    """fp64 attention of q [B, Hq, D] over the first prefix_len rows of the
+    prefix caches (codes [1, Hkv, P, D], ...) and each sequence's own first
+    lengths[b] rows; zeros where a sequence has no row at all."""
+    def rows(cache, b, h, n):
+        c, s, z = cache
+        return (c[b, h, :n].astype(np.float64) - z[b, h, :n].astype(np.float64)[:, None]) * \
+            s[b, h, :n].astype(np.float64)[:, None]
+    q = np.asarray(q, np.float64)
+    b_, hq, d = q.shape
+    hkv = k_cache[0].shape[1]
+    r = hq // hkv
+    out = np.zeros_like(q)
+    for h in range(hkv):
+        kp, vp = rows(prefix_k, 0, h, prefix_len), rows(prefix_v, 0, h, prefix_len)
+        for b in range(b_):
+            k = np.concatenate([kp, rows(k_cache, b, h, lengths[b])])
+            v = np.concatenate([vp, rows(v_cache, b, h, lengths[b])])
+            if len(k) == 0:
+                continue
+            s = q[b, h * r:(h + 1) * r] @ k.T / np.sqrt(d)
+            e = np.exp(s - s.max(axis=1, keepdims=True))
+            out[b, h * r:(h + 1) * r] = (e @ v) / e.sum(axis=1, keepdims=True)
+    return out

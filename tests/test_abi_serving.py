@@ -51,3 +51,35 @@ def test_kv_rows_validation(wq, call):
     for bad in (dict(d=64), dict(t=2 ** 31), dict(cap=2 ** 31 - 1), dict(b=65536),
                 dict(t=2 ** 31 - 1, h=9)):
         assert call(wq, **bad) == wq.WQ_ERR_UNSUPPORTED, bad
+
+
+def _attn(wq, q=A16, dt=0, stride=1024, b=2, hq=8, hkv=2, d=128, p=24, pcap=24, pre=(A16,) * 6,
+          cap=16, own=(A16,) * 6, ln=A16, out=A16, ws=A16, n=1 << 40):
+    return wq.lib.wq_prefix_attention(q, dt, stride, b, hq, hkv, d, p, pcap, *pre, cap, *own, ln,
+                                      out, ws, n, None)
+
+
+def test_prefix_attention_validation(wq):
+    assert _attn(wq, b=0) == wq.WQ_OK
+    for bad in (dict(b=-1), dict(hq=0), dict(hkv=0), dict(hq=9), dict(d=0), dict(p=-1), dict(cap=0),
+                dict(p=25), dict(dt=2), dict(stride=-8), dict(q=None), dict(ln=None),
+                dict(out=None), dict(pre=(None,) * 6), dict(own=(A16,) * 5 + (None,))):
+        assert _attn(wq, **bad) == wq.WQ_ERR_INVALID_ARG, bad
+    for bad in (dict(d=64), dict(hq=34), dict(cap=2 ** 31 - 1), dict(p=2 ** 31 - 1, pcap=2 ** 31),
+                dict(pcap=2 ** 31 - 1), dict(b=2 ** 28)):
+        assert _attn(wq, **bad) == wq.WQ_ERR_UNSUPPORTED, bad
+    for bad in (dict(q=MIS), dict(out=MIS), dict(ln=A16 + 2), dict(stride=1028), dict(ws=MIS),
+                dict(pre=(A16, MIS) + (A16,) * 4), dict(own=(MIS,) + (A16,) * 5)):
+        assert _attn(wq, **bad) == wq.WQ_ERR_ALIGNMENT, bad
+    assert _attn(wq, ws=None) == wq.WQ_ERR_WORKSPACE
+    size = ctypes.c_size_t()
+    assert wq.lib.wq_prefix_attention_workspace(2, 8, 2, 128, 24, 16, ctypes.byref(size)) == wq.WQ_OK
+    assert size.value > 0
+    assert _attn(wq, n=size.value - 1) == wq.WQ_ERR_WORKSPACE
+    assert wq.lib.wq_prefix_attention_workspace(0, 8, 2, 128, 24, 16,
+                                                ctypes.byref(size)) == wq.WQ_OK
+    assert size.value == 0
+    assert wq.lib.wq_prefix_attention_workspace(2, 8, 2, 64, 24, 16,
+                                                ctypes.byref(size)) == wq.WQ_ERR_UNSUPPORTED
+    assert wq.lib.wq_prefix_attention_workspace(2, 8, 2, 128, 24, 16, None) == \
+        wq.WQ_ERR_INVALID_ARG
