@@ -32,6 +32,7 @@ WQ_OP_GEMV = 0
 WQ_OP_GEMM = 1
 WQ_OP_MSD_GEMM = 2
 WQ_OP_MX_GEMV = 3
+WQ_OP_MX_GEMM = 4
 
 # every symbol include/wq.h declares
 EXPORTED = [
@@ -43,7 +44,7 @@ EXPORTED = [
     "wq_test_set_wait", "wq_mx_quantize", "wq_mx_decompose", "wq_mx_gemv", "wq_msd_gemm_nf4",
     "wq_msd_decode_attention", "wq_msd_decode_attention_workspace",
     "wq_test_set_attention_split", "wq_kv_block_values", "wq_kv_append", "wq_kv_read",
-    "wq_prefix_attention", "wq_prefix_attention_workspace",
+    "wq_prefix_attention", "wq_prefix_attention_workspace", "wq_mx_quantize_planes", "wq_mx_gemm",
 ]
 
 _DTYPES = {torch.bfloat16: WQ_BF16, torch.float16: WQ_FP16, torch.float32: WQ_FP32}
@@ -100,6 +101,8 @@ def _load():
                                  P, I64, P, P, P, P, P, P, P, P, P, SZ, P], ctypes.c_int),
         "wq_prefix_attention_workspace": ([I64, I64, I64, I32, I64, I64, ctypes.POINTER(SZ)],
                                           ctypes.c_int),
+        "wq_mx_quantize_planes": ([P, ctypes.c_int, I64, I64, I64, I32, P, P, P], ctypes.c_int),
+        "wq_mx_gemm": ([P, P, I64, I64, I64, I32, P, P, P, P, SZ, P], ctypes.c_int),
         "wq_msd_gemm_noalloc": ([P, I64, I64, I64, I32, I32, P, P, P, P, P], ctypes.c_int),
         "wq_residual": ([ctypes.c_int, P, I64, I64, I32, P, P, P, P, P], ctypes.c_int),
         "wq_select_salient": ([P, I64, I64, I32, P, P], ctypes.c_int),
@@ -433,6 +436,65 @@ def wq_mx_gemv(x, n, n_passes, codes, scales, workspace=None, out=None, stream=N
         out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_mx_gemv(_ptr(x), m, n, k, n_passes, _ptr(codes), _ptr(scales), _ptr(out),
                           _ptr(workspace), workspace.numel(), _stream(stream)), "wq_mx_gemv")
+    return out
+
+
+def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
+    """MXFP4 activations kept in 4 bits: x [M, K] (bf16, fp16 or fp32; rows may
+    be strided) -> (planes uint8 [P, M, K/2], scale bytes uint8 [P, M, K/32])."""
+    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16, float16 or float32 CUDA tensor")
+    m, k = x.shape
+    if x.stride(1) != 1 and k > 1:
+        raise ValueError("the rows of x must be contiguous")
+    if planes is None:
+        planes = torch.empty(n_planes, m, k // 2, dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty(n_planes, m, k // 32, dtype=torch.uint8, device=x.device)
+    _cuda(planes, torch.uint8, "planes")
+    _cuda(scales, torch.uint8, "scales")
+    if planes.shape != (n_planes, m, k // 2) or scales.shape != (n_planes, m, k // 32):
+        raise ValueError("planes must be [%d, %d, %d] and scales [%d, %d, %d]"
+                         % (n_planes, m, k // 2, n_planes, m, k // 32))
+    _on_current_device(x, planes, scales)
+    _check(lib.wq_mx_quantize_planes(_ptr(x), _DTYPES[x.dtype], max(x.stride(0), k) if m < 2
+                                     else x.stride(0), m, k, n_planes, _ptr(planes), _ptr(scales),
+                                     _stream(stream)), "wq_mx_quantize_planes")
+    return planes, scales
+
+
+def mx_gemm_workspace(m, n, k, n_planes=2, device="cuda"):
+    nbytes = wq_workspace_bytes(WQ_OP_MX_GEMM, m, n, k, 0, n_planes)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
+def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None, stream=None):
+    """y bf16 [M, N] = (sum of the MXFP4 planes) . w_hat^T for any M, on the FP4
+    tensor cores: planes and plane_scales as wq_mx_quantize_planes returns
+    them, codes and scales as wq_mx_quantize packs the weights [N, K]."""
+    for t, name in ((planes, "planes"), (plane_scales, "plane_scales"), (codes, "codes"),
+                    (scales, "scales")):
+        _cuda(t, torch.uint8, name)
+    if planes.dim() != 3:
+        raise ValueError("planes must be [P, M, K/2]")
+    p, m, kh = planes.shape
+    k = 2 * kh
+    if plane_scales.shape != (p, m, k // 32) or codes.shape != (n, kh) or \
+            scales.shape != (n, k // 32):
+        raise ValueError("scales or weights do not match planes %s and N = %d"
+                         % (tuple(planes.shape), n))
+    if workspace is None:
+        workspace = mx_gemm_workspace(m, n, k, p, planes.device)
+    if out is None:
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=planes.device)
+    _cuda(out, torch.bfloat16, "y")
+    if out.shape != (m, n):
+        raise ValueError("y must be [%d, %d]" % (m, n))
+    _on_current_device(planes, plane_scales, codes, scales, workspace, out)
+    _check(lib.wq_mx_gemm(_ptr(planes), _ptr(plane_scales), m, n, k, p, _ptr(codes), _ptr(scales),
+                          _ptr(out), _ptr(workspace),
+                          workspace.numel() * workspace.element_size(), _stream(stream)),
+           "wq_mx_gemm")
     return out
 
 

@@ -45,6 +45,12 @@ wq_status launch_kv_append(const void*, const void*, wq_dtype, int64_t, int64_t,
 wq_status launch_kv_read(void*, void*, wq_dtype, int64_t, int64_t, const int64_t*, const int64_t*,
                          int64_t, const int32_t*, const int32_t*, int64_t, const void* const*,
                          cudaStream_t);
+wq_status launch_mx_planes(const void*, wq_dtype, int64_t, int64_t, int64_t, int32_t, uint8_t*,
+                           uint8_t*, cudaStream_t);
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t P);
+wq_status launch_mx_gemm(const uint8_t*, const uint8_t*, int64_t, int64_t, int64_t, int32_t,
+                         const uint8_t*, const uint8_t*, void*, void*, cudaStream_t);
+wq_status read_mx_gemm_error(bool clear, uint32_t* v);
 size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap);
 wq_status launch_prefix_attn(const void*, wq_dtype, int64_t, int64_t, int64_t, int64_t, int64_t,
                              int64_t, const void* const*, int64_t, const void* const*,
@@ -456,6 +462,44 @@ wq_status wq_mx_gemv(const void* x, int64_t M, int64_t N, int64_t K, int32_t n_p
   });
 }
 
+wq_status wq_mx_quantize_planes(const void* x, wq_dtype dtype, int64_t ldx, int64_t M, int64_t K,
+                                int32_t n_planes, uint8_t* codes, uint8_t* scales, void* stream) {
+  if (M < 0 || K <= 0 || K % 32 != 0 || ldx < K) return WQ_ERR_INVALID_ARG;
+  if (n_planes != 1 && n_planes != 2) return WQ_ERR_INVALID_ARG;
+  if (dtype != WQ_BF16 && dtype != WQ_FP16 && dtype != WQ_FP32) return WQ_ERR_INVALID_ARG;
+  if (M == 0) return WQ_OK;
+  if (!x || !codes || !scales) return WQ_ERR_INVALID_ARG;
+  if (!all_aligned({x, codes, scales}) || ldx % (dtype == WQ_FP32 ? 4 : 8) != 0)
+    return WQ_ERR_ALIGNMENT;
+  if (M > INT32_MAX || K > INT32_MAX - 255) return WQ_ERR_UNSUPPORTED;
+  return guarded([&] {
+    return launch_mx_planes(x, dtype, ldx, M, K, n_planes, codes, scales, as_stream(stream));
+  });
+}
+
+wq_status wq_mx_gemm(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t N, int64_t K,
+                     int32_t n_planes, const uint8_t* w_codes, const uint8_t* w_scales, void* y,
+                     void* workspace, size_t ws_bytes, void* stream) {
+  if (M < 0 || N < 0 || K <= 0 || K % 32 != 0) return WQ_ERR_INVALID_ARG;
+  if (n_planes != 1 && n_planes != 2) return WQ_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return WQ_OK;
+  if (!codes || !scales || !w_codes || !w_scales || !y) return WQ_ERR_INVALID_ARG;
+  if (!all_aligned({codes, scales, w_codes, w_scales, y})) return WQ_ERR_ALIGNMENT;
+  if (K % 128 != 0 || N % 16 != 0) return WQ_ERR_UNSUPPORTED;
+  // token rows of all planes and feature rows are tensor coordinates, tiles
+  // are counted in 32 bits
+  if (M > (1 << 29) || N > (1 << 30) || K > (1 << 30) ||
+      ((M + 127) / 128) * ((N + 63) / 64) > INT32_MAX)
+    return WQ_ERR_UNSUPPORTED;
+  const size_t need = mx_gemm_workspace_bytes(M, N, K, n_planes);
+  if (need > 0 && (!workspace || ws_bytes < need)) return WQ_ERR_WORKSPACE;
+  if (!all_aligned({workspace})) return WQ_ERR_ALIGNMENT;
+  return guarded([&] {
+    return launch_mx_gemm(codes, scales, M, N, K, n_planes, w_codes, w_scales, y, workspace,
+                          as_stream(stream));
+  });
+}
+
 wq_status wq_kv_block_values(const uint32_t* codes, int64_t rows, int64_t L, int32_t D,
                              uint32_t* out, void* stream) {
   if (rows < 0 || L <= 0 || D <= 0 || D % 8 != 0) return WQ_ERR_INVALID_ARG;
@@ -573,7 +617,6 @@ wq_status wq_msd_decode_attention(const void* q, int64_t B, int64_t Hq, int64_t 
 
 wq_status wq_workspace_bytes(wq_op op, int64_t M, int64_t N, int64_t K, int32_t group,
                              int32_t n_components, size_t* bytes) {
-  (void)N;
   (void)group;
   if (!bytes || M < 0 || K < 0) return WQ_ERR_INVALID_ARG;
   switch (op) {
@@ -590,6 +633,10 @@ wq_status wq_workspace_bytes(wq_op op, int64_t M, int64_t N, int64_t K, int32_t 
     case WQ_OP_MX_GEMV:
       if (n_components != 1 && n_components != 2) return WQ_ERR_INVALID_ARG;
       *bytes = M == 0 ? 0 : mx_workspace_bytes(M, K, n_components);
+      return WQ_OK;
+    case WQ_OP_MX_GEMM:
+      if (N < 0 || (n_components != 1 && n_components != 2)) return WQ_ERR_INVALID_ARG;
+      *bytes = M == 0 || N == 0 ? 0 : mx_gemm_workspace_bytes(M, N, K, n_components);
       return WQ_OK;
   }
   return WQ_ERR_INVALID_ARG;
@@ -611,15 +658,17 @@ wq_status wq_test_set_attention_split(int32_t chunks_per_cta) {
 wq_status wq_device_error(void* stream, int clear, uint32_t* detail) {
   return guarded([&] {
     if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return WQ_ERR_CUDA;
-    uint32_t a = 0, b = 0, c = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0;
     wq_status s = read_gemm_error(clear != 0, &a);
     if (s != WQ_OK) return s;
     s = read_msd_error(clear != 0, &b);
     if (s != WQ_OK) return s;
     s = read_gemv_error(clear != 0, &c);
     if (s != WQ_OK) return s;
-    if (detail) *detail = a ? a : (b ? b : c);
-    return (a || b || c) ? WQ_ERR_TIMEOUT : WQ_OK;
+    s = read_mx_gemm_error(clear != 0, &d);
+    if (s != WQ_OK) return s;
+    if (detail) *detail = a ? a : (b ? b : (c ? c : d));
+    return (a || b || c || d) ? WQ_ERR_TIMEOUT : WQ_OK;
   });
 }
 

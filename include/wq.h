@@ -82,7 +82,9 @@ typedef enum {
 
 typedef enum { WQ_FMT_INT4_ASYM = 0, WQ_FMT_NF4 = 1 } wq_format;
 typedef enum { WQ_BF16 = 0, WQ_FP16 = 1, WQ_FP32 = 2 } wq_dtype;
-typedef enum { WQ_OP_GEMV = 0, WQ_OP_GEMM = 1, WQ_OP_MSD_GEMM = 2, WQ_OP_MX_GEMV = 3 } wq_op;
+typedef enum {
+  WQ_OP_GEMV = 0, WQ_OP_GEMM = 1, WQ_OP_MSD_GEMM = 2, WQ_OP_MX_GEMV = 3, WQ_OP_MX_GEMM = 4
+} wq_op;
 
 /* Human-readable name of a status. Never NULL. Host only. */
 const char* wq_status_string(wq_status status);
@@ -369,6 +371,37 @@ wq_status wq_mx_gemv(const void* x, int64_t M, int64_t N, int64_t K, int32_t n_p
                      size_t ws_bytes, void* stream);
 
 /*
+ * MXFP4 activations kept in 4 bits, and their product with MXFP4 weights for
+ * any number of tokens, on the block-scaled FP4 tensor cores ([MSD]: MXFP4
+ * passes of the activations multiply the MXFP4 weights directly).
+ *
+ * wq_mx_quantize_planes: x [M, K] (bf16, fp16 or fp32; row m at m * ldx
+ *   elements, rows 16-byte aligned, ldx >= K) -> n_planes (1 or 2) MXFP4 planes
+ *   codes uint8 [n_planes][M][K/2] (element 2j in the low nibble of byte j)
+ *   and scale bytes uint8 [n_planes][M][K/32], by the rules of wq_mx_decompose
+ *   with n_passes == 2: plane 0 = MXFP4(x), plane 1 = MXFP4(x - plane 0). The
+ *   values are those of wq_mx_decompose's planes; one quantization serves every
+ *   product of the same activations. K % 32 == 0; M == 0 is a no-op. Bit-exact
+ *   with the oracle for finite x; non-finite x gives unspecified codes in its
+ *   block.
+ * wq_mx_gemm: y bf16 [M, N] = (sum of the planes) . w_hat^T for any M, with
+ *   codes/scales as above and the weights as wq_mx_quantize packs them
+ *   (w_codes [N, K/2], w_scales [N, K/32]). Products of two blocks are exact
+ *   in the tensor core and accumulate in fp32; one rounding to bf16. M == 0 or
+ *   N == 0: no-op. Requires K % 128 == 0 and N % 16 == 0. Scale bytes of 255
+ *   are NaN. Workspace: at least wq_workspace_bytes(WQ_OP_MX_GEMM, M, N, K, 0,
+ *   n_planes) bytes (may be 0: then NULL is taken); contents on entry do not
+ *   matter. May return WQ_ERR_TIMEOUT through wq_device_error if an internal
+ *   bounded wait expires.
+ * Both are asynchronous on `stream`; every buffer is caller-owned.
+ */
+wq_status wq_mx_quantize_planes(const void* x, wq_dtype dtype, int64_t ldx, int64_t M, int64_t K,
+                                int32_t n_planes, uint8_t* codes, uint8_t* scales, void* stream);
+wq_status wq_mx_gemm(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t N, int64_t K,
+                     int32_t n_planes, const uint8_t* w_codes, const uint8_t* w_scales, void* y,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Multi-Scale Dequant in decode attention over an INT4 KV cache ([MSD],
  * Abstract: the quantized KV cache multiplies low-precision components of
  * the other operand directly, so the cache is never dequantized and its HBM
@@ -522,7 +555,8 @@ wq_status wq_msd_decode_attention_workspace(int64_t B, int64_t Hq, int64_t Hkv, 
 
 /*
  * Workspace bytes an entry point needs for the given problem (0 if none);
- * for WQ_OP_MX_GEMV, n_components is the number of passes (1 or 2).
+ * for WQ_OP_MX_GEMV, n_components is the number of passes (1 or 2), for
+ * WQ_OP_MX_GEMM the number of planes (1 or 2).
  * Host only; `bytes` is a host pointer.
  */
 wq_status wq_workspace_bytes(wq_op op, int64_t M, int64_t N, int64_t K,
@@ -533,8 +567,8 @@ wq_status wq_workspace_bytes(wq_op op, int64_t M, int64_t N, int64_t K,
  * Test hook for the bounded device waits. The pages have no counterpart: it
  * exists so that the timeout path can be exercised without a device fault.
  * It applies to every later launch, in this process, of the kernels with
- * bounded waits (the tensor-core kernels of wq_w4a16_gemm, and of
- * wq_msd_gemm for M > 16):
+ * bounded waits (the tensor-core kernels of wq_w4a16_gemm, of wq_mx_gemm, and
+ * of wq_msd_gemm for M > 16):
  *   limit_ns  how long any one device wait may last before the kernel gives
  *             up; 0 restores the default of 2 s;
  *   stall     1: the kernel's loader withholds the first k-tile, so the first
