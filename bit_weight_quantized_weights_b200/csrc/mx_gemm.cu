@@ -40,28 +40,47 @@ __device__ __forceinline__ int e2m1_exponent(float a) {
   return max(e, -127);
 }
 
-// Eight E2M1 codes of f[i] * scale, element i in nibble i; zeros are +0.
+// Eight E2M1 codes of f[i] * scale, element i in nibble i (a negative value
+// that rounds to zero has code 8 here).
 __device__ __forceinline__ uint32_t e2m1_x8(const float (&f)[8], float scale) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint16_t b;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u16.u8 %0, t;\n\t}"
-        : "=h"(b)
-        : "f"(f[2 * i + 1] * scale), "f"(f[2 * i] * scale));
-    w |= (uint32_t)b << (8 * i);
-  }
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(f[0] * scale), "f"(f[1] * scale), "f"(f[2] * scale), "f"(f[3] * scale),
+        "f"(f[4] * scale), "f"(f[5] * scale), "f"(f[6] * scale), "f"(f[7] * scale));
+  return w;
+}
+
+// Code 8 to code 0: zeros are +0.
+__device__ __forceinline__ uint32_t plus_zero(uint32_t w) {
   const uint32_t some = (w | (w >> 1) | (w >> 2)) & 0x11111111u;  // magnitude above 0
   return w & (0x77777777u | (some << 3));
 }
 
-// The value of one code: E2M1 magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t mag = c & 7u;
-  // codes 2..7 are 2^((c >> 1) - 1) (1 + (c & 1) / 2); 0 and 1 are 0 and 1/2
-  const uint32_t norm = (((mag >> 1) + 126u) << 23) | ((mag & 1u) << 22);
-  const uint32_t bits = mag < 2 ? (mag ? 0x3F000000u : 0u) : norm;
-  return __uint_as_float(bits | ((c & 8u) << 28));
+// The values of eight codes. (The conversion is given bytes of a word's low half
+// only: from the third and fourth byte of an unpacked word, nvcc 12.9 returned
+// zeros.)
+__device__ __forceinline__ void e2m1_values(uint32_t w, float (&v)[8]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+        : "=r"(h[2 * i]), "=r"(h[2 * i + 1])
+        : "r"(w >> (16 * i)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = t.x;
+    v[2 * i + 1] = t.y;
+  }
 }
 
 template <typename T>
@@ -120,31 +139,79 @@ __global__ void __launch_bounds__(256)
       const uint32_t w = e2m1_x8(f, pow2f(-e));
       if (in) {
         const int64_t row = (int64_t)p * M + m;
-        *reinterpret_cast<uint32_t*>(codes + (row * K + k) / 2) = w;
+        *reinterpret_cast<uint32_t*>(codes + (row * K + k) / 2) = plus_zero(w);
         if ((lane & 3) == 0) scales[(row * K + k) / 32] = (uint8_t)(e + 127);
       }
       if (p + 1 < PL) {
         const float up = pow2f(e);
+        float v[8];
+        e2m1_values(w, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = fmaf(-e2m1_value(w >> (4 * j)), up, f[j]);  // exact
+        for (int j = 0; j < 8; ++j) f[j] = fmaf(-v[j], up, f[j]);  // exact
       }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
+// Scale bytes [rows][K / 32] to the order the MMA takes them in, a 512-byte
+// piece for 128 rows x 4 scales (128 k): the 4 bytes of row r at byte
+// (r % 32) * 16 + (r / 32) * 4, i.e. lane r % 32, column r / 32 of 4 TMEM
+// columns. Pieces are ordered [row block][k / 256][2], zeros (the scale 2^-127)
+// where there is no row or block. Loading the bytes a row at a time inside the
+// product cost it as much as its MMAs (one 4-byte request a row and 128 k);
+// this pass moves K N / 32 bytes once.
+// ---------------------------------------------------------------------------
+struct ScaleArgs {
+  const uint8_t* xs;  // [P][M][K / 32]
+  const uint8_t* ws;  // [N][K / 32]
+  uint8_t* out;       // pieces of x's row blocks (by plane), then w's
+  int M, N, K, P;
+  int xblocks;        // ceil(M / 128)
+  int kt;             // ceil(K / 256)
+  int chunks;         // CTAs along k: ceil(2 kt / 8)
+};
+
+__global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
+  __shared__ __align__(16) uint32_t sm[8][128];  // piece, then word (r % 32) * 4 + r / 32
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int chunk = blockIdx.x % a.chunks, block = blockIdx.x / a.chunks;
+  const int words = a.K / 128;  // 4-byte groups of a row
+  const bool is_x = block < a.P * a.xblocks;
+  const int p = is_x ? block / a.xblocks : 0;
+  const int rb = is_x ? block - p * a.xblocks : block - a.P * a.xblocks;
+  const int nrows = is_x ? a.M : a.N;
+  const uint8_t* base = is_x ? a.xs + (int64_t)p * a.M * (a.K / 32) : a.ws;
+  const int r = threadIdx.x >> 1, g0 = (threadIdx.x & 1) * 4;  // row, first of 4 groups
+  const int row = rb * 128 + r;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(base + (int64_t)row * (a.K / 32));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = chunk * 8 + g0 + i;
+    sm[g0 + i][(r & 31) * 4 + (r >> 5)] = row < nrows && g < words ? src[g] : 0u;
+  }
+  __syncthreads();
+  const int piece = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (chunk * 8 + piece < 2 * a.kt)
+    *reinterpret_cast<uint4*>(a.out + (((int64_t)block * 2 * a.kt + chunk * 8 + piece) * 512) +
+                              16 * lane) = *reinterpret_cast<const uint4*>(&sm[piece][4 * lane]);
+}
+
+// ---------------------------------------------------------------------------
 // Product. A tile is 128 tokens (the MMA's M) by BN features (its N), summed
 // over all planes in one TMEM accumulator: a weight tile is loaded once and
 // multiplied with every plane's token tile. A stage holds 256 k (128-byte rows
-// of 4-bit codes, 128-byte swizzle) of all operands and their scale bytes,
-// which a warpgroup places in the order that tcgen05.cp copies to TMEM: 4 scale
-// bytes (128 k) of row r at byte (r % 32) * 16 + (r / 32) * 4 of a 512-byte
-// piece, one piece for 128 rows.
+// of 4-bit codes, 128-byte swizzle) of all operands.
 //   warp 0       TMA loads of the codes
-//   warp 1       tcgen05.cp of the scales, tcgen05.mma (one thread)
-//   warps 4-7    scale bytes into shared memory (4-byte cp.async)
+//   warp 1       tcgen05.mma (one thread)
+//   warps 4-7    scales: one 16-byte load a lane and piece, tcgen05.st to a ring
+//                of TMEM columns (every warp writes its lane quarter: the MMA
+//                reads the scales from all four). tcgen05.cp from shared memory
+//                by the MMA's thread took a fifth of the MMAs' time.
 //   warps 8-15   epilogue: TMEM to registers as packed bf16, which frees the
-//                accumulator for the next tile, then the stores
+//                accumulator for the next tile, then through shared memory to
+//                TMA stores (rows of 128 bytes; one 16-byte store a token cost
+//                70 us of 350 at 8192 x 14336 x 4096)
 // CTAs are persistent and take every gridDim.x-th tile.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128;
@@ -155,15 +222,21 @@ template <int BN, int PL>
 struct MxCfg {
   static constexpr int kXBytes = PL * kBM * kBKBytes;
   static constexpr int kWBytes = BN * kBKBytes;
-  static constexpr int kWPieces = (BN + 127) / 128;           // 128-row scale pieces
-  static constexpr int kSfBytes = (PL + kWPieces) * 2 * 512;  // two pieces a row block: 256 k
-  static constexpr int kStageBytes = kXBytes + kWBytes + kSfBytes;
-  static constexpr int kStages = 212992 / kStageBytes < 8 ? 212992 / kStageBytes : 8;
-  static constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
-  // TMEM columns: the accumulator, then two sets of scales (4 columns a piece)
+  static constexpr int kStageBytes = kXBytes + kWBytes;
+  static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
+  static constexpr int kEpiCols = BN / (kEpiWarps / 4);       // features a warp takes
+  static constexpr int kStageOut = 32 * 128;                  // a warp's 32 tokens x 64 features
+  static constexpr int kOutBytes = kEpiWarps * kStageOut;
+  static constexpr int kMaxStages = (232448 - 1024 - 512 - kOutBytes) / kStageBytes;
+  static constexpr int kStages = kMaxStages < 8 ? kMaxStages : 8;
+  static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + 512;
+  // TMEM columns: the accumulator, then the ring of scales (4 columns a piece)
+  static constexpr int kWPieces = (BN + 127) / 128;
   static constexpr int kSfCols = (PL + kWPieces) * 2 * 4;
-  static constexpr int kCols = BN + 2 * kSfCols;
+  static constexpr int kSfRing = 4;
+  static constexpr int kCols = BN + kSfRing * kSfCols;
   static constexpr int kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512, "TMEM columns");
 };
 
 // kind::mxf4: E2M1 x E2M1 with UE8M0 scales of blocks of 32, fp32 sums.
@@ -185,26 +258,15 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// A 512-byte scale piece (32 rows of 16 bytes, no swizzle: groups of 8 rows
-// 128 bytes apart) to 4 TMEM columns, the same in all four lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
-  const uint64_t desc = (uint64_t)((smem & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) |
-                        ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool in) {
-  // a size of 0 writes zeros: the scale 2^-127 of an operand that is zero
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(in ? 4 : 0)
-               : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+      : "memory");
 }
 
 struct MxArgs {
-  const uint8_t* xs;  // [PL][M][K / 32]
-  const uint8_t* ws;  // [N][K / 32]
-  uint16_t* y;
+  const uint8_t* sf;  // scale pieces of the token blocks (by plane), then of the weights
   int M, N, K;
   int mt, tiles;      // token tiles; all tiles
 };
@@ -212,19 +274,21 @@ struct MxArgs {
 template <int BN, int PL>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x,
-                   const __grid_constant__ CUtensorMap tmap_w, const MxArgs a, const WaitCtl wc) {
+                   const __grid_constant__ CUtensorMap tmap_w,
+                   const __grid_constant__ CUtensorMap tmap_y, const MxArgs a, const WaitCtl wc) {
   using Cfg = MxCfg<BN, PL>;
-  constexpr int S = Cfg::kStages;
+  constexpr int S = Cfg::kStages, F = Cfg::kSfRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint8_t* sx = smem;                       // [stage][plane][128 rows]
   uint8_t* sw = sx + S * Cfg::kXBytes;      // [stage][BN rows]
-  uint8_t* ssf = sw + S * Cfg::kWBytes;     // [stage][plane or weight piece][2][512]
-  uint64_t* full = reinterpret_cast<uint64_t*>(ssf + S * Cfg::kSfBytes);
-  uint64_t* sffull = full + S;
-  uint64_t* empty = sffull + S;
-  uint64_t* acc_full = empty + S;
+  uint8_t* sout = sw + S * Cfg::kWBytes;    // [epilogue warp][32 rows of 128 bytes]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sout + Cfg::kOutBytes);
+  uint64_t* empty = full + S;
+  uint64_t* sffull = empty + S;
+  uint64_t* sfempty = sffull + F;
+  uint64_t* acc_full = sfempty + F;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* mma_done = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -236,13 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     sm100::tma_prefetch_desc(&tmap_x);
     sm100::tma_prefetch_desc(&tmap_w);
+    sm100::tma_prefetch_desc(&tmap_y);
     for (int s = 0; s < S; ++s) {
       sm100::mbar_init(&full[s], 1);
-      sm100::mbar_init(&sffull[s], 128);
       sm100::mbar_init(&empty[s], 1);
     }
+    for (int f = 0; f < F; ++f) {
+      sm100::mbar_init(&sffull[f], 4);
+      sm100::mbar_init(&sfempty[f], 1);
+    }
     sm100::mbar_init(acc_full, 1);
-    sm100::mbar_init(acc_empty, 8);
+    sm100::mbar_init(acc_empty, Cfg::kEpiWarps);
     sm100::mbar_init(mma_done, 1);
     *abort_flag = 0;
     sm100::fence_mbar_init();
@@ -296,37 +364,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm100::tc_fence_after();
         }
         for (int kt = 0; kt < KT; ++kt, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (uint32_t)(it / S) & 1u;
-          if (!sm100::mbar_wait(&full[s], ph, &g_mx_gemm_error, 0x3202u, abort_flag,
-                                wc.limit_ns) ||
-              !sm100::mbar_wait(&sffull[s], ph, &g_mx_gemm_error, 0x3203u, abort_flag,
-                                wc.limit_ns)) {
+          const int s = it % S, f = it % F;
+          if (!sm100::mbar_wait(&full[s], (uint32_t)(it / S) & 1u, &g_mx_gemm_error, 0x3202u,
+                                abort_flag, wc.limit_ns) ||
+              !sm100::mbar_wait(&sffull[f], (uint32_t)(it / F) & 1u, &g_mx_gemm_error, 0x3203u,
+                                abort_flag, wc.limit_ns)) {
             ok = false;
             break;
           }
           sm100::tc_fence_after();
-          // scales of the stage: two sets of TMEM columns in turn, so that a
-          // copy never meets the MMAs of the stage before
-          const uint32_t sf = tmem_sf + (uint32_t)(it & 1) * Cfg::kSfCols;
-          const uint32_t sf_smem = smem_u32(ssf + s * Cfg::kSfBytes);
-#pragma unroll
-          for (int i = 0; i < PL + Cfg::kWPieces; ++i)
-#pragma unroll
-            for (int kg = 0; kg < 2; ++kg) {
-              // weights: the two pieces of 128 rows of one kg side by side
-              const uint32_t col =
-                  i < PL ? (i * 2 + kg) * 4
-                         : PL * 8 + kg * 4 * Cfg::kWPieces + (i - PL) * 4;
-              copy_scales(sf + col, sf_smem + (uint32_t)(i * 2 + kg) * 512);
-            }
+          const uint32_t sf = tmem_sf + (uint32_t)f * Cfg::kSfCols;
           const uint32_t xb = smem_u32(sx + s * Cfg::kXBytes);
           const uint32_t wb = smem_u32(sw + s * Cfg::kWBytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 64 k each: 32 bytes, 2 scale bytes
             const int kg = kk >> 1;
-            const uint32_t idesc =
-                (kk & 1) ? idesc_mxf4(BN, 2) : idesc_mxf4(BN, 0);
+            const uint32_t idesc = (kk & 1) ? idesc_mxf4(BN, 2) : idesc_mxf4(BN, 0);
             const uint64_t bdesc = sm100::sdesc_sw128_kmajor(wb + kk * 32);
             const uint32_t sfb = sf + PL * 8 + kg * 4 * Cfg::kWPieces;
 #pragma unroll
@@ -335,62 +388,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                        idesc, sf + (p * 2 + kg) * 4, sfb, (kt | kk | p) != 0 ? 1u : 0u);
           }
           sm100::mma_commit(&empty[s]);
+          sm100::mma_commit(&sfempty[f]);
         }
         if (ok) sm100::mma_commit(acc_full);
       }
       sm100::mma_commit(mma_done);
     }
   } else if (warp >= 4 && warp < 8) {
-    // ---------------- scale bytes: thread = row of a 128-row block ----------------
-    const int r = threadIdx.x - 128;
-    const int K32 = a.K / 32;
-    const uint32_t dst0 = smem_u32(ssf) + (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
+    // ---------------- scales ----------------
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are complete
+    constexpr int kPieces = Cfg::kSfCols / 4;
+    const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+    const int64_t wbase = (int64_t)PL * a.mt * KT * 2;  // pieces before the weights'
+    // the pieces of one stage in column order: planes (2 of k each), then the
+    // weights' by k
+    auto load = [&](uint4 (&v)[kPieces], int t, int kt) {
+      const int mb = t % a.mt, n0 = (t / a.mt) * BN;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        int64_t at;
+        if (i < 2 * PL) {
+          at = (((int64_t)(i >> 1) * a.mt + mb) * KT + kt) * 2 + (i & 1);
+        } else {
+          const int j = i - 2 * PL, kg = j / Cfg::kWPieces, wp = j % Cfg::kWPieces;
+          // a block of 128 features past N has no pieces: its columns are not stored
+          const int nb = min(n0 / 128 + wp, (a.N - 1) / 128);
+          at = wbase + ((int64_t)nb * KT + kt) * 2 + kg;
+        }
+        v[i] = *reinterpret_cast<const uint4*>(a.sf + at * 512 + 16 * lane);
+        // 64 features from the middle of a block of 128: rows 64 .. 127 are columns 2, 3
+        if (BN == 64 && i >= 2 * PL && (n0 & 64)) v[i] = make_uint4(v[i].z, v[i].w, 0u, 0u);
+      }
+    };
+    uint4 v[kPieces];
+    if (blockIdx.x < a.tiles) load(v, blockIdx.x, 0);
     int it = 0;
     bool ok = true;
-    auto publish = [&](int i) {  // the writes of stage i are complete
-      sm100::fence_proxy_async_smem();
-      sm100::mbar_arrive(&sffull[i % S]);
-    };
     for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-      const int m0 = (t % a.mt) * kBM, n0 = (t / a.mt) * BN;
       for (int kt = 0; kt < KT; ++kt, ++it) {
-        const int s = it % S;
-        if (it >= S && !sm100::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u, &g_mx_gemm_error,
-                                         0x3301u, abort_flag, wc.limit_ns)) {
-          ok = false;
-          break;
-        }
-        const uint32_t dst = dst0 + (uint32_t)s * Cfg::kSfBytes;
-#pragma unroll
-        for (int i = 0; i < PL + Cfg::kWPieces; ++i) {
-          bool in = i < PL ? m0 + r < a.M : n0 + (i - PL) * 128 + r < a.N;
-          if (BN < 128 && i >= PL) in = in && r < BN;
-          const int64_t row = !in ? 0
-                              : i < PL ? (int64_t)i * a.M + m0 + r
-                                       : (int64_t)n0 + (i - PL) * 128 + r;
-          const uint8_t* src = (i < PL ? a.xs : a.ws) + row * K32 + kt * 8;
-#pragma unroll
-          for (int kg = 0; kg < 2; ++kg) {
-            const bool have = in && kt * 8 + kg * 4 < K32;
-            cp_async4(dst + (uint32_t)(i * 2 + kg) * 512, have ? src + kg * 4 : a.ws, have);
+        const int f = it % F;
+        if (it >= F) {
+          const bool got = sm100::mbar_wait(&sfempty[f], (uint32_t)(it / F - 1) & 1u,
+                                            &g_mx_gemm_error, 0x3301u, abort_flag, wc.limit_ns);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
           }
+          sm100::tc_fence_after();
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (it > 0) {
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-          publish(it - 1);
-        }
+#pragma unroll
+        for (int i = 0; i < kPieces; i += 2)
+          tmem_st8(tmem_sf + quarter + (uint32_t)(f * Cfg::kSfCols + 4 * i), v[i], v[i + 1]);
+        // the next stage's pieces are on their way while these are stored
+        if (kt + 1 < KT)
+          load(v, t, kt + 1);
+        else if (t + (int)gridDim.x < a.tiles)
+          load(v, t + gridDim.x, 0);
+        sm100::tmem_st_wait();
+        sm100::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sffull[f]);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok && it > 0) publish(it - 1);
-  } else if (warp >= 8) {
-    // ---------------- epilogue: thread = token, half of the tile's features ----------------
+  } else if (warp >= 8 && warp < 8 + Cfg::kEpiWarps) {
+    // ---------------- epilogue: thread = token, kEpiCols of the tile's features ----------------
     const int q = warp & 3, part = (warp - 8) >> 2;
-    constexpr int kCols = BN / 2;
+    constexpr int kCols = Cfg::kEpiCols;
+    uint8_t* buf = sout + (warp - 8) * Cfg::kStageOut;
     int n = 0;
     for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n) {
-      const int m = (t % a.mt) * kBM + 32 * q + lane;
+      const int m0 = (t % a.mt) * kBM + 32 * q;
       const int col0 = (t / a.mt) * BN + part * kCols;
       const bool got = sm100::mbar_wait(acc_full, (uint32_t)n & 1u, &g_mx_gemm_error, 0x3401u,
                                         abort_flag, wc.limit_ns);
@@ -409,15 +476,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(acc_empty);
-      if (m < a.M) {
-        uint16_t* dst = a.y + (int64_t)m * a.N + col0;
 #pragma unroll
-        for (int i = 0; i < kCols / 8; ++i)
-          if (col0 + 8 * i < a.N)
-            *reinterpret_cast<uint4*>(dst + 8 * i) =
-                make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+      for (int c = 0; c < kCols / 64; ++c) {
+        // 16-byte chunk i of token row `lane` sits at chunk i ^ (lane % 8) (128-byte swizzle)
+        if (lane == 0) sm100::bulk_wait_read_all();  // the store before has left the buffer
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+              make_uint4(out[32 * c + 4 * i], out[32 * c + 4 * i + 1], out[32 * c + 4 * i + 2],
+                         out[32 * c + 4 * i + 3]);
+        sm100::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && m0 < a.M && col0 + 64 * c < a.N) {
+          sm100::tma_store_2d(&tmap_y, buf, col0 + 64 * c, m0);  // clipped at M and N
+          sm100::bulk_commit();
+        }
       }
     }
+    if (lane == 0) sm100::bulk_wait_all();
   }
 
   // After an abort: wait (bounded) for the loads and MMAs still in flight.
@@ -436,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int BN, int PL>
-wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, const MxArgs& a0,
-                        cudaStream_t st) {
+wq_status launch_gemm_t(const CUtensorMap& tx, const CUtensorMap& ty, const void* wcodes,
+                        const MxArgs& a0, cudaStream_t st) {
   using Cfg = MxCfg<BN, PL>;
   CUtensorMap tw;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, wcodes, (uint64_t)a0.K / 2,
@@ -449,27 +526,36 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, const MxArgs&
   }();
   if (!attr_set) return WQ_ERR_CUDA;
   MxArgs a = a0;
-  a.mt = (a.M + kBM - 1) / kBM;
   a.tiles = a.mt * ((a.N + BN - 1) / BN);
-  mx_gemm_kernel<BN, PL><<<std::min(a.tiles, num_sms()), kThreads, Cfg::kSmem, st>>>(tx, tw, a,
-                                                                                    wait_ctl());
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  cfg.gridDim = dim3((unsigned)std::min(a.tiles, num_sms()), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, PL>, tx, tw, ty, a, wait_ctl()) != cudaSuccess)
+    return WQ_ERR_CUDA;
   return launch_status();
 }
 
 template <int PL>
-wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, const MxArgs& a,
-                      cudaStream_t st) {
+wq_status launch_gemm(const CUtensorMap& tx, const CUtensorMap& ty, const void* wcodes,
+                      const MxArgs& a, cudaStream_t st) {
   // the tile width with the least time for the slowest CTA: whole tiles an SM
   // takes, times a tile's cost
-  const int64_t mt = (a.M + kBM - 1) / kBM, sms = num_sms();
+  const int64_t mt = a.mt, sms = num_sms();
   auto cost = [&](int bn, int64_t tile) {
     const int64_t tiles = mt * ((a.N + bn - 1) / bn);
     return (tiles + sms - 1) / sms * tile;
   };
   const int64_t c64 = cost(64, 90), c128 = cost(128, 140), c256 = cost(256, 256);
-  if (c256 <= c128 && c256 <= c64) return launch_gemm_t<256, PL>(tx, wcodes, a, st);
-  if (c128 <= c64) return launch_gemm_t<128, PL>(tx, wcodes, a, st);
-  return launch_gemm_t<64, PL>(tx, wcodes, a, st);
+  if (c256 <= c128 && c256 <= c64) return launch_gemm_t<256, PL>(tx, ty, wcodes, a, st);
+  if (c128 <= c64) return launch_gemm_t<128, PL>(tx, ty, wcodes, a, st);
+  return launch_gemm_t<64, PL>(tx, ty, wcodes, a, st);
 }
 
 template <typename T>
@@ -496,24 +582,43 @@ wq_status launch_mx_planes(const void* x, wq_dtype dt, int64_t ldx, int64_t M, i
   return launch_status();
 }
 
-size_t mx_gemm_workspace_bytes(int64_t, int64_t, int64_t, int32_t) { return 0; }
+// Workspace: the scale pieces of all planes' token blocks and of the weights'
+// feature blocks.
+size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t P) {
+  return (size_t)(P * ((M + 127) / 128) + (N + 127) / 128) * ((K + 255) / 256) * 1024;
+}
 
 wq_status launch_mx_gemm(const uint8_t* xc, const uint8_t* xs, int64_t M, int64_t N, int64_t K,
-                         int32_t P, const uint8_t* wc, const uint8_t* ws, void* y, void*,
+                         int32_t P, const uint8_t* wc, const uint8_t* ws, void* y, void* workspace,
                          cudaStream_t st) {
-  CUtensorMap tx;
+  CUtensorMap tx, ty;
   if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xc, (uint64_t)K / 2, (uint64_t)(P * M),
                     (uint64_t)K / 2, kBKBytes, kBM, CU_TENSOR_MAP_SWIZZLE_128B))
     return WQ_ERR_CUDA;
+  if (!make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, (uint64_t)N, (uint64_t)M,
+                    (uint64_t)N * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return WQ_ERR_CUDA;
+  ScaleArgs sa;
+  sa.xs = xs;
+  sa.ws = ws;
+  sa.out = static_cast<uint8_t*>(workspace);
+  sa.M = (int)M;
+  sa.N = (int)N;
+  sa.K = (int)K;
+  sa.P = P;
+  sa.xblocks = (int)((M + 127) / 128);
+  sa.kt = (int)((K + 255) / 256);
+  sa.chunks = (2 * sa.kt + 7) / 8;
+  const int64_t blocks = (int64_t)P * sa.xblocks + (N + 127) / 128;
+  mx_scales_kernel<<<(unsigned)(blocks * sa.chunks), 256, 0, st>>>(sa);
   MxArgs a;
-  a.xs = xs;
-  a.ws = ws;
-  a.y = static_cast<uint16_t*>(y);
+  a.sf = sa.out;
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
-  a.mt = a.tiles = 0;
-  return P == 1 ? launch_gemm<1>(tx, wc, a, st) : launch_gemm<2>(tx, wc, a, st);
+  a.mt = sa.xblocks;
+  a.tiles = 0;
+  return P == 1 ? launch_gemm<1>(tx, ty, wc, a, st) : launch_gemm<2>(tx, ty, wc, a, st);
 }
 
 wq_status read_mx_gemm_error(bool clear, uint32_t* v) {

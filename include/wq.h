@@ -390,8 +390,7 @@ wq_status wq_mx_gemv(const void* x, int64_t M, int64_t N, int64_t K, int32_t n_p
  *   in the tensor core and accumulate in fp32; one rounding to bf16. M == 0 or
  *   N == 0: no-op. Requires K % 128 == 0 and N % 16 == 0. Scale bytes of 255
  *   are NaN. Workspace: at least wq_workspace_bytes(WQ_OP_MX_GEMM, M, N, K, 0,
- *   n_planes) bytes (may be 0: then NULL is taken); contents on entry do not
- *   matter. May return WQ_ERR_TIMEOUT through wq_device_error if an internal
+ *   n_planes) bytes; contents on entry do not matter. May return WQ_ERR_TIMEOUT through wq_device_error if an internal
  *   bounded wait expires.
  * Both are asynchronous on `stream`; every buffer is caller-owned.
  */
