@@ -489,7 +489,7 @@ wq_status wq_mx_gemm(const uint8_t* codes, const uint8_t* scales, int64_t M, int
   // token rows of all planes and feature rows are tensor coordinates, tiles
   // are counted in 32 bits
   if (M > (1 << 29) || N > (1 << 30) || K > (1 << 30) ||
-      ((M + 127) / 128) * ((N + 63) / 64) > INT32_MAX ||
+      ((M + 127) / 128) * ((N + 31) / 32) > INT32_MAX ||
       ((M + 63) / 64 + N / 128 + 2) * (K / 1024 + 1) > INT32_MAX)
     return WQ_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < mx_gemm_workspace_bytes(M, N, K, n_planes)) return WQ_ERR_WORKSPACE;

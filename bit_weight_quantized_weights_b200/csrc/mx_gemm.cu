@@ -203,7 +203,10 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 // multiplied with every plane's token tile. A stage holds 256 k (128-byte rows
 // of 4-bit codes, 128-byte swizzle) of all operands.
 //   warp 0       TMA loads of the codes
-//   warp 1       tcgen05.mma (one thread)
+//   warp 1       tcgen05.mma: the whole warp runs the loop and one elected lane
+//                issues, so that the operands' addresses are warp-uniform (a
+//                loop of one lane spent 90 cycles an MMA moving them to the
+//                uniform registers the instruction takes: 1100 cycles a stage)
 //   warps 4-7    scales: one 16-byte load a lane and piece, tcgen05.st to a ring
 //                of TMEM columns (every warp writes its lane quarter: the MMA
 //                reads the scales from all four). tcgen05.cp from shared memory
@@ -225,7 +228,8 @@ struct MxCfg {
   static constexpr int kStageBytes = kXBytes + kWBytes;
   static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
   static constexpr int kEpiCols = BN / (kEpiWarps / 4);       // features a warp takes
-  static constexpr int kStageOut = 32 * 128;                  // a warp's 32 tokens x 64 features
+  static constexpr int kChunk = BN < 64 ? BN : 64;            // features of one store
+  static constexpr int kStageOut = 32 * kChunk * 2;           // a warp's 32 tokens x kChunk
   static constexpr int kOutBytes = kEpiWarps * kStageOut;
   static constexpr int kMaxStages = (232448 - 1024 - 512 - kOutBytes) / kStageBytes;
   static constexpr int kStages = kMaxStages < 8 ? kMaxStages : 8;
@@ -233,8 +237,10 @@ struct MxCfg {
   // TMEM columns: the accumulator, then the ring of scales (4 columns a piece)
   static constexpr int kWPieces = (BN + 127) / 128;
   static constexpr int kSfCols = (PL + kWPieces) * 2 * 4;
-  static constexpr int kSfRing = 4;
-  static constexpr int kCols = BN + kSfRing * kSfCols;
+  // stages whose scales are on their way in registers (32 registers a stage at
+  // most): one stage ahead cost 0.55 us a stage, the latency of the loads
+  static constexpr int kSfAhead = BN >= 256 ? 2 : 3;
+  static constexpr int kCols = BN + kStages * kSfCols;
   static constexpr int kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "TMEM columns");
 };
@@ -258,6 +264,26 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
+// sm100::sdesc_sw128_kmajor in halves: the low word holds the address (16-byte
+// units, advanced by adding), the high word is constant.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint64_t sdesc_at(uint32_t lo) {
+  return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -269,6 +295,7 @@ struct MxArgs {
   const uint8_t* sf;  // scale pieces of the token blocks (by plane), then of the weights
   int M, N, K;
   int mt, tiles;      // token tiles; all tiles
+  int xrows;          // token rows a TMA load brings: 128, or M rounded up to 8
 };
 
 template <int BN, int PL>
@@ -277,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmap_w,
                    const __grid_constant__ CUtensorMap tmap_y, const MxArgs a, const WaitCtl wc) {
   using Cfg = MxCfg<BN, PL>;
-  constexpr int S = Cfg::kStages, F = Cfg::kSfRing;
+  constexpr int S = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -287,8 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sout + Cfg::kOutBytes);
   uint64_t* empty = full + S;
   uint64_t* sffull = empty + S;
-  uint64_t* sfempty = sffull + F;
-  uint64_t* acc_full = sfempty + F;
+  uint64_t* acc_full = sffull + S;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* mma_done = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -304,10 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < S; ++s) {
       sm100::mbar_init(&full[s], 1);
       sm100::mbar_init(&empty[s], 1);
-    }
-    for (int f = 0; f < F; ++f) {
-      sm100::mbar_init(&sffull[f], 4);
-      sm100::mbar_init(&sfempty[f], 1);
+      sm100::mbar_init(&sffull[s], 4);
     }
     sm100::mbar_init(acc_full, 1);
     sm100::mbar_init(acc_empty, Cfg::kEpiWarps);
@@ -327,108 +350,131 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int last_issued = -1;
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-        const int m0 = (t % a.mt) * kBM, n0 = (t / a.mt) * BN;
-        for (int kt = 0; kt < KT; ++kt, ++it) {
-          const int s = it % S;
-          if (it >= S && !sm100::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u,
-                                           &g_mx_gemm_error, 0x3101u, abort_flag, wc.limit_ns)) {
-            ok = false;
-            break;
-          }
-          if (wc.stall && it == 0) continue;  // test hook: the first k-tile never arrives
-          last_issued = it;
-          sm100::mbar_arrive_expect_tx(&full[s], Cfg::kXBytes + Cfg::kWBytes);
+    int it = 0;
+    bool ok = true;
+    const uint32_t bytes = (uint32_t)(PL * a.xrows * kBKBytes) + Cfg::kWBytes;
+    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+      const int m0 = (t % a.mt) * kBM, n0 = (t / a.mt) * BN;
+      for (int kt = 0; kt < KT; ++kt, ++it) {
+        const int s = it % S;
+        if (it >= S) {
+          ok = __all_sync(0xffffffffu,
+                          sm100::mbar_wait(&empty[s], (uint32_t)(it / S - 1) & 1u,
+                                           &g_mx_gemm_error, 0x3101u, abort_flag, wc.limit_ns));
+          if (!ok) break;
+        }
+        if (wc.stall && it == 0) continue;  // test hook: the first k-tile never arrives
+        last_issued = it;
+        if (elect_one()) {
+          sm100::mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
           for (int p = 0; p < PL; ++p)
             sm100::tma_load_2d(sx + s * Cfg::kXBytes + p * kBM * kBKBytes, &tmap_x, &full[s],
                                kt * kBKBytes, p * a.M + m0);
           sm100::tma_load_2d(sw + s * Cfg::kWBytes, &tmap_w, &full[s], kt * kBKBytes, n0);
         }
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int it = 0, n = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n) {
-        if (n > 0) {
-          if (!sm100::mbar_wait(acc_empty, (uint32_t)(n - 1) & 1u, &g_mx_gemm_error, 0x3201u,
-                                abort_flag, wc.limit_ns)) {
-            ok = false;
-            break;
-          }
-          sm100::tc_fence_after();
-        }
-        for (int kt = 0; kt < KT; ++kt, ++it) {
-          const int s = it % S, f = it % F;
-          if (!sm100::mbar_wait(&full[s], (uint32_t)(it / S) & 1u, &g_mx_gemm_error, 0x3202u,
-                                abort_flag, wc.limit_ns) ||
-              !sm100::mbar_wait(&sffull[f], (uint32_t)(it / F) & 1u, &g_mx_gemm_error, 0x3203u,
-                                abort_flag, wc.limit_ns)) {
-            ok = false;
-            break;
-          }
-          sm100::tc_fence_after();
-          const uint32_t sf = tmem_sf + (uint32_t)f * Cfg::kSfCols;
-          const uint32_t xb = smem_u32(sx + s * Cfg::kXBytes);
-          const uint32_t wb = smem_u32(sw + s * Cfg::kWBytes);
+    const uint32_t xlo0 = uniform(sdesc_lo(smem_u32(sx))), wlo0 = uniform(sdesc_lo(smem_u32(sw)));
+    const uint32_t tm = uniform(tmem);
+    int it = 0, n = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n) {
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu,
+                        sm100::mbar_wait(acc_empty, (uint32_t)(n - 1) & 1u, &g_mx_gemm_error,
+                                         0x3201u, abort_flag, wc.limit_ns));
+        if (!ok) break;
+        sm100::tc_fence_after();
+      }
+      for (int kt = 0; kt < KT; ++kt, ++it) {
+        const int s = it % S;
+        const uint32_t ph = (uint32_t)(it / S) & 1u;
+        ok = __all_sync(0xffffffffu, sm100::mbar_wait(&full[s], ph, &g_mx_gemm_error, 0x3202u,
+                                                      abort_flag, wc.limit_ns) &&
+                                         sm100::mbar_wait(&sffull[s], ph, &g_mx_gemm_error,
+                                                          0x3203u, abort_flag, wc.limit_ns));
+        if (!ok) break;
+        sm100::tc_fence_after();
+        const uint32_t sf = tm + BN + (uint32_t)(s * Cfg::kSfCols);
+        const uint32_t xlo = xlo0 + (uint32_t)(s * (Cfg::kXBytes >> 4));
+        const uint32_t wlo = wlo0 + (uint32_t)(s * (Cfg::kWBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 64 k each: 32 bytes, 2 scale bytes
             const int kg = kk >> 1;
             const uint32_t idesc = (kk & 1) ? idesc_mxf4(BN, 2) : idesc_mxf4(BN, 0);
-            const uint64_t bdesc = sm100::sdesc_sw128_kmajor(wb + kk * 32);
             const uint32_t sfb = sf + PL * 8 + kg * 4 * Cfg::kWPieces;
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-              mma_mxf4(tmem, sm100::sdesc_sw128_kmajor(xb + p * kBM * kBKBytes + kk * 32), bdesc,
-                       idesc, sf + (p * 2 + kg) * 4, sfb, (kt | kk | p) != 0 ? 1u : 0u);
+              mma_mxf4(tm, sdesc_at(xlo + p * (kBM * kBKBytes >> 4) + kk * 2),
+                       sdesc_at(wlo + kk * 2), idesc, sf + (p * 2 + kg) * 4, sfb,
+                       (kk | p) != 0 || kt != 0 ? 1u : 0u);
           }
           sm100::mma_commit(&empty[s]);
-          sm100::mma_commit(&sfempty[f]);
+          if (kt == KT - 1) sm100::mma_commit(acc_full);
         }
-        if (ok) sm100::mma_commit(acc_full);
+        __syncwarp();
       }
-      sm100::mma_commit(mma_done);
     }
+    if (elect_one()) sm100::mma_commit(mma_done);
+    __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // ---------------- scales ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are complete
     constexpr int kPieces = Cfg::kSfCols / 4;
     const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
-    const int64_t wbase = (int64_t)PL * a.mt * KT * 2;  // pieces before the weights'
     // the pieces of one stage in column order: planes (2 of k each), then the
-    // weights' by k
-    auto load = [&](uint4 (&v)[kPieces], int t, int kt) {
-      const int mb = t % a.mt, n0 = (t / a.mt) * BN;
+    // weights' by k. They are 1024 bytes (2 pieces) after the stage before's.
+    constexpr int D = Cfg::kSfAhead;
+    const int mine = blockIdx.x < a.tiles ? (a.tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    const int total = mine * KT;  // stages of this CTA
+    const uint8_t *px[PL], *pw[Cfg::kWPieces];
+    int lt = blockIdx.x, lk = 0;  // the next stage to load
+    auto next = [&](uint4 (&v)[kPieces]) {
+      if (lk == 0) {
+        const int mb = lt % a.mt, n0 = (lt / a.mt) * BN;
+#pragma unroll
+        for (int p = 0; p < PL; ++p)
+          px[p] = a.sf + (int64_t)(p * a.mt + mb) * KT * 1024 + 16 * lane;
+#pragma unroll
+        for (int w = 0; w < Cfg::kWPieces; ++w)
+          // a block of 128 features past N has no pieces: its columns are not stored
+          pw[w] = a.sf + (int64_t)(PL * a.mt + min(n0 / 128 + w, (a.N - 1) / 128)) * KT * 1024 +
+                  16 * lane;
+      }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        int64_t at;
-        if (i < 2 * PL) {
-          at = (((int64_t)(i >> 1) * a.mt + mb) * KT + kt) * 2 + (i & 1);
-        } else {
-          const int j = i - 2 * PL, kg = j / Cfg::kWPieces, wp = j % Cfg::kWPieces;
-          // a block of 128 features past N has no pieces: its columns are not stored
-          const int nb = min(n0 / 128 + wp, (a.N - 1) / 128);
-          at = wbase + ((int64_t)nb * KT + kt) * 2 + kg;
-        }
-        v[i] = *reinterpret_cast<const uint4*>(a.sf + at * 512 + 16 * lane);
-        // 64 features from the middle of a block of 128: rows 64 .. 127 are columns 2, 3
-        if (BN == 64 && i >= 2 * PL && (n0 & 64)) v[i] = make_uint4(v[i].z, v[i].w, 0u, 0u);
+        const int j = i - 2 * PL;
+        v[i] = *reinterpret_cast<const uint4*>(
+            i < 2 * PL ? px[i >> 1] + 512 * (i & 1)
+                       : pw[j % Cfg::kWPieces] + 512 * (j / Cfg::kWPieces));
+      }
+#pragma unroll
+      for (int p = 0; p < PL; ++p) px[p] += 1024;
+#pragma unroll
+      for (int w = 0; w < Cfg::kWPieces; ++w) pw[w] += 1024;
+      if (++lk == KT) {
+        lk = 0;
+        lt += gridDim.x;
       }
     };
-    uint4 v[kPieces];
-    if (blockIdx.x < a.tiles) load(v, blockIdx.x, 0);
-    int it = 0;
+    uint4 v[D][kPieces];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (d < total) next(v[d]);
     bool ok = true;
-    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-      for (int kt = 0; kt < KT; ++kt, ++it) {
-        const int f = it % F;
-        if (it >= F) {
-          const bool got = sm100::mbar_wait(&sfempty[f], (uint32_t)(it / F - 1) & 1u,
+    int st = blockIdx.x, sk = 0, c = 0;  // the stage being stored
+    for (int base = 0; base < total && ok; base += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int it = base + d;
+        if (it >= total || !ok) break;
+        const int f = it % S;
+        if (it >= S) {
+          const bool got = sm100::mbar_wait(&empty[f], (uint32_t)(it / S - 1) & 1u,
                                             &g_mx_gemm_error, 0x3301u, abort_flag, wc.limit_ns);
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
@@ -436,14 +482,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           sm100::tc_fence_after();
         }
+        if (BN < 128) {
+          // a tile inside a block of 128 features: rows 32 c .. are column c
+          if (sk == 0) c = ((st / a.mt) * BN & 127) / 32;
+#pragma unroll
+          for (int i = 2 * PL; i < kPieces; ++i) {
+            if (c & 2) v[d][i] = make_uint4(v[d][i].z, v[d][i].w, 0u, 0u);
+            if (c & 1) v[d][i].x = v[d][i].y;
+          }
+          if (++sk == KT) {
+            sk = 0;
+            st += gridDim.x;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < kPieces; i += 2)
-          tmem_st8(tmem_sf + quarter + (uint32_t)(f * Cfg::kSfCols + 4 * i), v[i], v[i + 1]);
-        // the next stage's pieces are on their way while these are stored
-        if (kt + 1 < KT)
-          load(v, t, kt + 1);
-        else if (t + (int)gridDim.x < a.tiles)
-          load(v, t + gridDim.x, 0);
+          tmem_st8(tmem_sf + quarter + (uint32_t)(f * Cfg::kSfCols + 4 * i), v[d][i], v[d][i + 1]);
+        if (it + D < total) next(v[d]);
         sm100::tmem_st_wait();
         sm100::tc_fence_before();
         __syncwarp();
@@ -476,20 +531,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(acc_empty);
+      constexpr int kChunk = Cfg::kChunk;
 #pragma unroll
-      for (int c = 0; c < kCols / 64; ++c) {
-        // 16-byte chunk i of token row `lane` sits at chunk i ^ (lane % 8) (128-byte swizzle)
+      for (int c = 0; c < kCols / kChunk; ++c) {
+        // 16-byte piece i of token row `lane`, in the store's swizzle: rows of
+        // 128 bytes have piece i at i ^ (row % 8), of 64 bytes at i ^ (row / 2 % 4)
+        const int sw = kChunk == 64 ? lane & 7 : (lane >> 1) & 3;
         if (lane == 0) sm100::bulk_wait_read_all();  // the store before has left the buffer
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-              make_uint4(out[32 * c + 4 * i], out[32 * c + 4 * i + 1], out[32 * c + 4 * i + 2],
-                         out[32 * c + 4 * i + 3]);
+        for (int i = 0; i < kChunk / 8; ++i) {
+          const uint32_t* o = out + kChunk / 2 * c + 4 * i;
+          *reinterpret_cast<uint4*>(buf + lane * kChunk * 2 + ((i ^ sw) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
         sm100::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && m0 < a.M && col0 + 64 * c < a.N) {
-          sm100::tma_store_2d(&tmap_y, buf, col0 + 64 * c, m0);  // clipped at M and N
+        if (lane == 0 && m0 < a.M && col0 + kChunk * c < a.N) {
+          sm100::tma_store_2d(&tmap_y, buf, col0 + kChunk * c, m0);  // clipped at M and N
           sm100::bulk_commit();
         }
       }
@@ -513,10 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int BN, int PL>
-wq_status launch_gemm_t(const CUtensorMap& tx, const CUtensorMap& ty, const void* wcodes,
-                        const MxArgs& a0, cudaStream_t st) {
+wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a0,
+                        cudaStream_t st) {
   using Cfg = MxCfg<BN, PL>;
-  CUtensorMap tw;
+  CUtensorMap tw, ty;
+  if (!make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, (uint64_t)a0.N, (uint64_t)a0.M,
+                    (uint64_t)a0.N * 2, Cfg::kChunk, 32,
+                    Cfg::kChunk == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return WQ_ERR_CUDA;
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, wcodes, (uint64_t)a0.K / 2,
                     (uint64_t)a0.N, (uint64_t)a0.K / 2, kBKBytes, BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return WQ_ERR_CUDA;
@@ -543,8 +606,8 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const CUtensorMap& ty, const void
 }
 
 template <int PL>
-wq_status launch_gemm(const CUtensorMap& tx, const CUtensorMap& ty, const void* wcodes,
-                      const MxArgs& a, cudaStream_t st) {
+wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a,
+                      cudaStream_t st) {
   // the tile width with the least time for the slowest CTA: whole tiles an SM
   // takes, times a tile's cost
   const int64_t mt = a.mt, sms = num_sms();
@@ -552,10 +615,11 @@ wq_status launch_gemm(const CUtensorMap& tx, const CUtensorMap& ty, const void* 
     const int64_t tiles = mt * ((a.N + bn - 1) / bn);
     return (tiles + sms - 1) / sms * tile;
   };
-  const int64_t c64 = cost(64, 90), c128 = cost(128, 140), c256 = cost(256, 256);
-  if (c256 <= c128 && c256 <= c64) return launch_gemm_t<256, PL>(tx, ty, wcodes, a, st);
-  if (c128 <= c64) return launch_gemm_t<128, PL>(tx, ty, wcodes, a, st);
-  return launch_gemm_t<64, PL>(tx, ty, wcodes, a, st);
+  const int64_t c32 = cost(32, 70), c64 = cost(64, 90), c128 = cost(128, 140), c256 = cost(256, 256);
+  if (c256 <= std::min({c128, c64, c32})) return launch_gemm_t<256, PL>(tx, wcodes, y, a, st);
+  if (c128 <= std::min(c64, c32)) return launch_gemm_t<128, PL>(tx, wcodes, y, a, st);
+  if (c64 <= c32) return launch_gemm_t<64, PL>(tx, wcodes, y, a, st);
+  return launch_gemm_t<32, PL>(tx, wcodes, y, a, st);
 }
 
 template <typename T>
@@ -591,12 +655,12 @@ size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t P) {
 wq_status launch_mx_gemm(const uint8_t* xc, const uint8_t* xs, int64_t M, int64_t N, int64_t K,
                          int32_t P, const uint8_t* wc, const uint8_t* ws, void* y, void* workspace,
                          cudaStream_t st) {
-  CUtensorMap tx, ty;
+  // with fewer than 128 tokens the rest of the tile's rows is not loaded: an
+  // MMA row depends on its own operand row only, and rows past M are not stored
+  const int xrows = (int)std::min<int64_t>(kBM, (M + 7) / 8 * 8);
+  CUtensorMap tx;
   if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, xc, (uint64_t)K / 2, (uint64_t)(P * M),
-                    (uint64_t)K / 2, kBKBytes, kBM, CU_TENSOR_MAP_SWIZZLE_128B))
-    return WQ_ERR_CUDA;
-  if (!make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, (uint64_t)N, (uint64_t)M,
-                    (uint64_t)N * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+                    (uint64_t)K / 2, kBKBytes, (uint32_t)xrows, CU_TENSOR_MAP_SWIZZLE_128B))
     return WQ_ERR_CUDA;
   ScaleArgs sa;
   sa.xs = xs;
@@ -618,7 +682,8 @@ wq_status launch_mx_gemm(const uint8_t* xc, const uint8_t* xs, int64_t M, int64_
   a.K = (int)K;
   a.mt = sa.xblocks;
   a.tiles = 0;
-  return P == 1 ? launch_gemm<1>(tx, ty, wc, a, st) : launch_gemm<2>(tx, ty, wc, a, st);
+  a.xrows = xrows;
+  return P == 1 ? launch_gemm<1>(tx, wc, y, a, st) : launch_gemm<2>(tx, wc, y, a, st);
 }
 
 wq_status read_mx_gemm_error(bool clear, uint32_t* v) {
