@@ -51,6 +51,7 @@ size_t mx_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t P);
 wq_status launch_mx_gemm(const uint8_t*, const uint8_t*, int64_t, int64_t, int64_t, int32_t,
                          const uint8_t*, const uint8_t*, void*, void*, cudaStream_t);
 wq_status read_mx_gemm_error(bool clear, uint32_t* v);
+wq_status read_prefix_error(bool clear, uint32_t* v);
 size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap);
 wq_status launch_prefix_attn(const void*, wq_dtype, int64_t, int64_t, int64_t, int64_t, int64_t,
                              int64_t, const void* const*, int64_t, const void* const*,
@@ -658,17 +659,16 @@ wq_status wq_test_set_attention_split(int32_t chunks_per_cta) {
 wq_status wq_device_error(void* stream, int clear, uint32_t* detail) {
   return guarded([&] {
     if (cudaStreamSynchronize(as_stream(stream)) != cudaSuccess) return WQ_ERR_CUDA;
-    uint32_t a = 0, b = 0, c = 0, d = 0;
-    wq_status s = read_gemm_error(clear != 0, &a);
-    if (s != WQ_OK) return s;
-    s = read_msd_error(clear != 0, &b);
-    if (s != WQ_OK) return s;
-    s = read_gemv_error(clear != 0, &c);
-    if (s != WQ_OK) return s;
-    s = read_mx_gemm_error(clear != 0, &d);
-    if (s != WQ_OK) return s;
-    if (detail) *detail = a ? a : (b ? b : (c ? c : d));
-    return (a || b || c || d) ? WQ_ERR_TIMEOUT : WQ_OK;
+    uint32_t word = 0;
+    for (auto read : {read_gemm_error, read_msd_error, read_gemv_error, read_mx_gemm_error,
+                      read_prefix_error}) {
+      uint32_t w = 0;
+      wq_status s = read(clear != 0, &w);
+      if (s != WQ_OK) return s;
+      if (word == 0) word = w;
+    }
+    if (detail) *detail = word;
+    return word ? WQ_ERR_TIMEOUT : WQ_OK;
   });
 }
 

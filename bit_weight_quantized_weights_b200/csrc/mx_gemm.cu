@@ -264,26 +264,6 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// sm100::sdesc_sw128_kmajor in halves: the low word holds the address (16-byte
-// units, advanced by adding), the high word is constant.
-__device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr) {
-  return ((addr & 0x3FFFFu) >> 4) | (1u << 16);
-}
-__device__ __forceinline__ uint64_t sdesc_at(uint32_t lo) {
-  return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
-}
-
-// One lane of the converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -365,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (wc.stall && it == 0) continue;  // test hook: the first k-tile never arrives
         last_issued = it;
-        if (elect_one()) {
+        if (sm100::elect_one()) {
           sm100::mbar_arrive_expect_tx(&full[s], bytes);
 #pragma unroll
           for (int p = 0; p < PL; ++p)
@@ -377,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    const uint32_t xlo0 = uniform(sdesc_lo(smem_u32(sx))), wlo0 = uniform(sdesc_lo(smem_u32(sw)));
-    const uint32_t tm = uniform(tmem);
+    const uint32_t xlo0 = sm100::uniform(sm100::sdesc_lo(smem_u32(sx))), wlo0 = sm100::uniform(sm100::sdesc_lo(smem_u32(sw)));
+    const uint32_t tm = sm100::uniform(tmem);
     int it = 0, n = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n) {
@@ -401,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sf = tm + BN + (uint32_t)(s * Cfg::kSfCols);
         const uint32_t xlo = xlo0 + (uint32_t)(s * (Cfg::kXBytes >> 4));
         const uint32_t wlo = wlo0 + (uint32_t)(s * (Cfg::kWBytes >> 4));
-        if (elect_one()) {
+        if (sm100::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // 64 k each: 32 bytes, 2 scale bytes
             const int kg = kk >> 1;
@@ -409,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sfb = sf + PL * 8 + kg * 4 * Cfg::kWPieces;
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-              mma_mxf4(tm, sdesc_at(xlo + p * (kBM * kBKBytes >> 4) + kk * 2),
-                       sdesc_at(wlo + kk * 2), idesc, sf + (p * 2 + kg) * 4, sfb,
+              mma_mxf4(tm, sm100::sdesc_at(xlo + p * (kBM * kBKBytes >> 4) + kk * 2),
+                       sm100::sdesc_at(wlo + kk * 2), idesc, sf + (p * 2 + kg) * 4, sfb,
                        (kk | p) != 0 || kt != 0 ? 1u : 0u);
           }
           sm100::mma_commit(&empty[s]);
@@ -419,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (elect_one()) sm100::mma_commit(mma_done);
+    if (sm100::elect_one()) sm100::mma_commit(mma_done);
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // ---------------- scales ----------------

@@ -22,51 +22,18 @@
 #include <algorithm>
 #include <cmath>
 
-#include "common.cuh"
+#include "prefix_attn.cuh"
 
 namespace wq {
+
+wq_status launch_prefix_tc(const PrefixArgs& a, int row_tiles, cudaStream_t st);
+
 namespace {
 
-constexpr int kD = 128;
+using namespace prefix;
+
 constexpr int kWarps = 4;            // warps of a CTA; each takes every 4th step of a range
 constexpr int kStep = 32;            // keys of a warp's step
-constexpr float kNone = -1e30f;      // the running bound before any key
-constexpr float kSlack = 8.0f;       // w may grow to 2^8 before the bound is moved
-
-struct Cache {
-  const uint32_t* kc;   // [.., cap, 16]
-  const __half* ks;     // [.., cap]
-  const __half* kz;
-  const uint32_t* vc;   // [.., nblk, 128]
-  const __half* vs;
-  const __half* vz;
-  int64_t cap;
-  int64_t nblk;
-};
-
-struct PrefixArgs {
-  const void* q;         // [B, Hq, 128], rows of a sequence q_stride elements apart
-  int64_t q_stride;
-  int fp16;              // q and out are fp16 (else bf16)
-  int B, Hq, Hkv, R;
-  Cache pre, own;
-  int P;
-  const int32_t* lengths;
-  int chunk_p, nsp;      // keys of a prefix range, ranges
-  int chunk_o, nso;      // keys of a range of own tokens, ranges
-  int nrt;               // prefix row tiles
-  int nprefix;           // CTAs of the prefix: Hkv * nrt * nsp
-  float* part;           // [B * Hq][nsp + nso][128]
-  float2* stat;          // [B * Hq][nsp + nso] (m, E)
-  void* out;
-};
-
-__device__ __forceinline__ float ex2(float x) {  // ex2.approx: 2^-22 relative; 2^-inf = 0
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -80,20 +47,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
-}
-
-__device__ __forceinline__ uint32_t h2(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
-__device__ __forceinline__ __half2 as_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
-
-// Codes of nibbles (0, 4) and (1, 5) of a word as exact fp16 integers q - z:
-// a nibble placed in the low mantissa bits of 1024 is 1024 + q, one place
-// higher 1024 + 16 q. z1024 = (1024 + z) of both keys, zm64 = -(64 + z).
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t z1024, uint32_t zm64, uint32_t& even,
-                                          uint32_t& odd) {
-  const uint32_t e = lop3_and_or(w, 0x000F000Fu, 0x64006400u);
-  const uint32_t o = lop3_and_or(w, 0x00F000F0u, 0x64006400u);
-  even = h2(__hsub2(as_h2(e), as_h2(z1024)));
-  odd = h2(__hfma2(as_h2(o), as_h2(0x2C002C00u), as_h2(zm64)));  // 0x2C00 = 1/16
 }
 
 // One step's 32 keys as they come from memory. Lane (g, t4) holds the K rows
@@ -187,12 +140,8 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
     for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(f[i]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // 2^e with amax 2^e in [2^14, 2^15); 1 for a row of zeros, infinities or
-    // magnitudes whose power of two is outside fp32's normal range
-    const int ex = (int)(__float_as_uint(amax) >> 23);
-    const bool scaled = ex > 14 && ex < 255;
-    const float up = scaled ? __uint_as_float((uint32_t)(127 + 14 + 127 - ex) << 23) : 1.0f;
-    const float down = scaled ? __uint_as_float((uint32_t)(ex - 14) << 23) : 1.0f;
+    float up, down;
+    row_scale(amax, up, down);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -200,7 +149,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
 #pragma unroll
         for (int b = 0; b < 2; ++b)
           bq[nt][2 * j + e][b] = pack_f16x2(f[8 * j + 2 * e + b] * up, f[8 * j + 2 * e + b + 4] * up);
-    const float fac = down * (float)(1.4426950408889634 / 11.313708498984761);  // log2(e)/sqrt(128)
+    const float fac = down * kScoreScale;
     cr[nt][0] = __shfl_sync(0xffffffffu, fac, (2 * t4) * 4);
     cr[nt][1] = __shfl_sync(0xffffffffu, fac, (2 * t4 + 1) * 4);
   }
@@ -410,14 +359,17 @@ __device__ __forceinline__ int own_length(const PrefixArgs& p, int b) {
   return min(max(p.lengths[b], 0), (int)p.own.cap);
 }
 
-// CTAs 0 .. nprefix - 1: key range x row tile x KV head of the prefix; the
-// rest: key range x KV head x sequence of the own tokens.
+// CTAs 0 .. nprefix - 1: key range x row tile x KV head of the prefix (none
+// where the tcgen05 kernel takes it: nprefix is 0 here); the rest: key range x
+// KV head x sequence of the own tokens. Launched while the tcgen05 kernel still
+// runs, whose results the merge needs too: every CTA ends by waiting for it.
 template <int NT>
-__global__ void __launch_bounds__(32 * kWarps) prefix_attn_kernel(const __grid_constant__ PrefixArgs p) {
+__global__ void __launch_bounds__(32 * kWarps)
+    prefix_attn_kernel(const __grid_constant__ PrefixArgs p, int nprefix) {
   __shared__ __align__(16) float sm[8 * NT * (kD + 4) + 2 * kWarps * 8 * NT];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int i = blockIdx.x;
-  if (i < p.nprefix) {
+  if (i < nprefix) {
     const int slot = i % p.nsp;
     const int rt = (i / p.nsp) % p.nrt;
     const int kh = i / (p.nsp * p.nrt);
@@ -425,17 +377,18 @@ __global__ void __launch_bounds__(32 * kWarps) prefix_attn_kernel(const __grid_c
     attend<NT>(p, p.pre, kh * p.pre.cap, kh * p.pre.nblk, kh, rt * 8 * NT,
                min(8 * NT, p.B * p.R - rt * 8 * NT), begin, min(begin + p.chunk_p, p.P), slot, sm);
   } else {
-    i -= p.nprefix;
+    i -= nprefix;
     const int range = i % p.nso;
     const int kh = (i / p.nso) % p.Hkv;
     const int b = i / (p.nso * p.Hkv);
     const int len = own_length(p, b);
     const int begin = range * p.chunk_o;
-    if (begin >= len) return;
     const int64_t bh = (int64_t)b * p.Hkv + kh;
-    attend<NT>(p, p.own, bh * p.own.cap, bh * p.own.nblk, kh, b * p.R, p.R, begin,
-               min(begin + p.chunk_o, len), p.nsp + range, sm);
+    if (begin < len)
+      attend<NT>(p, p.own, bh * p.own.cap, bh * p.own.nblk, kh, b * p.R, p.R, begin,
+                 min(begin + p.chunk_o, len), p.nsp + range, sm);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One warp a row: the ranges' partial results against their common bound.
@@ -454,6 +407,7 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const __grid_constant
   float e = 0.0f;
   for (int j = 0; j < n; ++j) {
     const float2 st = p.stat[base + j];
+    if (st.y == 0.0f) continue;  // a range without keys wrote no partial result
     const float f = ex2(st.x - big);
     const float4 v = *reinterpret_cast<const float4*>(p.part + (base + j) * kD + 4 * lane);
     a.x = fmaf(f, v.x, a.x);
@@ -474,39 +428,70 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const __grid_constant
 
 // How a problem is cut: the same for the workspace query and the launch.
 struct Plan {
-  int nt, nrt, chunk_p, nsp, chunk_o, nso;
+  int tc;  // row tiles of a tcgen05 CTA (1 or 2), or 0: the prefix on mma.sync
+  int nt, nrt, chunk_p, ranges, nsp, chunk_o, nso;
 };
 
 Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
   Plan pl;
-  const int64_t R = Hq / Hkv;
-  pl.nt = R <= 8 ? 1 : 2;
-  pl.nrt = (int)((B * R + 8 * pl.nt - 1) / (8 * pl.nt));
+  const int64_t R = Hq / Hkv, rows = B * R, sms = num_sms();
   const int64_t step = kWarps * kStep;
-  const int64_t want = (int64_t)num_sms() * 4;  // CTAs: four of a wave's fit an SM
+  const int64_t want = sms * 4;  // CTAs: four of a wave's fit an SM
   auto cut = [&](int64_t keys, int64_t others, int& chunk, int& n) {
     const int64_t ranges =
         std::max<int64_t>(1, std::min<int64_t>((keys + step - 1) / step, want / others));
     chunk = (int)(((keys + ranges - 1) / ranges + step - 1) / step * step);
     n = (int)((keys + chunk - 1) / chunk);
   };
-  cut(std::max<int64_t>(P, 1), std::max<int64_t>(1, Hkv * pl.nrt), pl.chunk_p, pl.nsp);
-  if (P == 0) pl.nsp = 0;
+  pl.nt = R <= 8 ? 1 : 2;
+  pl.tc = 0;
+  pl.nsp = pl.ranges = 0;
+  pl.nrt = 0;
+  pl.chunk_p = 128;
+  if (P > 0 && rows > 16) {
+    // tcgen05: the ranges that give the slowest SM the least work, a CTA's
+    // start and end counted as 4 tiles
+    const int64_t tiles = (P + 127) / 128, rt = (rows + 127) / 128;
+    pl.tc = rt >= 2 ? 2 : 1;
+    pl.nrt = (int)((rt + pl.tc - 1) / pl.tc);
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= std::min<int64_t>(tiles, 64); ++n) {
+      const int64_t waves = (Hkv * pl.nrt * n + sms - 1) / sms;
+      const int64_t cost = waves * ((tiles + n - 1) / n + 4);
+      if (cost < best) {
+        best = cost;
+        pl.chunk_p = (int)((tiles + n - 1) / n) * 128;
+      }
+    }
+    pl.ranges = (int)((P + pl.chunk_p - 1) / pl.chunk_p);
+    pl.nsp = pl.tc == 1 ? 2 * pl.ranges : pl.ranges;
+  } else if (P > 0) {
+    pl.nrt = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+    cut(P, std::max<int64_t>(1, Hkv * pl.nrt), pl.chunk_p, pl.ranges);
+    pl.nsp = pl.ranges;
+  }
   cut(cap, std::max<int64_t>(1, B * Hkv), pl.chunk_o, pl.nso);
   return pl;
 }
 
 template <int NT>
-wq_status launch(const PrefixArgs& a, cudaStream_t st) {
+wq_status launch(const PrefixArgs& a, int tc, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.stream = st;
-  cfg.gridDim = dim3((unsigned)(a.nprefix + (int64_t)a.nso * a.Hkv * a.B), 1, 1);
-  cfg.blockDim = dim3(32 * kWarps, 1, 1);
-  if (cudaLaunchKernelEx(&cfg, prefix_attn_kernel<NT>, a) != cudaSuccess) return WQ_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.stream = st;
+  if (tc) {
+    wq_status s = launch_prefix_tc(a, tc, st);
+    if (s != WQ_OK) return s;
+    cfg.numAttrs = 1;
+  }
+  const int nprefix = tc ? 0 : a.nprefix;
+  cfg.gridDim = dim3((unsigned)(nprefix + (int64_t)a.nso * a.Hkv * a.B), 1, 1);
+  cfg.blockDim = dim3(32 * kWarps, 1, 1);
+  if (cudaLaunchKernelEx(&cfg, prefix_attn_kernel<NT>, a, nprefix) != cudaSuccess)
+    return WQ_ERR_CUDA;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq + 3) / 4), 1, 1);
   cfg.blockDim = dim3(128, 1, 1);
@@ -549,11 +534,11 @@ wq_status launch_prefix_attn(const void* q, wq_dtype dt, int64_t q_stride, int64
   a.chunk_o = pl.chunk_o;
   a.nso = pl.nso;
   a.nrt = pl.nrt;
-  a.nprefix = (int)(Hkv * pl.nrt * pl.nsp);
+  a.nprefix = (int)(Hkv * pl.nrt * pl.ranges);
   a.part = static_cast<float*>(workspace);
   a.stat = reinterpret_cast<float2*>(a.part + (size_t)B * Hq * (pl.nsp + pl.nso) * kD);
   a.out = out;
-  return pl.nt == 1 ? launch<1>(a, st) : launch<2>(a, st);
+  return pl.nt == 1 ? launch<1>(a, pl.tc, st) : launch<2>(a, pl.tc, st);
 }
 
 }  // namespace wq

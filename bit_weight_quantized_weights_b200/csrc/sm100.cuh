@@ -203,6 +203,28 @@ __device__ __forceinline__ uint64_t sdesc_sw128_kmajor(uint32_t addr) {
   return d;
 }
 
+// The same descriptor in halves: the low word holds the address (16-byte units,
+// advanced by adding), the high word is constant.
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint64_t sdesc_at(uint32_t lo) {
+  return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+
+// One lane of the converged warp; and a value that is the same in every lane,
+// marked as such. tcgen05 and TMA instructions take warp-uniform operands:
+// issued by one elected lane of a warp that runs its loop as a whole, they cost
+// less than in a loop of one lane.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Instruction descriptors (dense, K-major A and B).
 //   bits 4-5 D type, 7-9 A type, 10-12 B type, 17-22 N/8, 24-28 M/16.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int m, int n) {

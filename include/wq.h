@@ -526,7 +526,8 @@ wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_ze
  * be NULL. prefix_cap or cap > 2^31 - 8, R > 16, B * Hq or B * R > 2^30 return
  * WQ_ERR_UNSUPPORTED. Workspace: at least wq_prefix_attention_workspace(...)
  * bytes for the same sizes; contents on entry do not matter, and calls that
- * may overlap on the GPU need one each. Asynchronous on `stream`.
+ * may overlap on the GPU need one each. May return WQ_ERR_TIMEOUT through
+ * wq_device_error if an internal bounded wait expires. Asynchronous on `stream`.
  */
 wq_status wq_prefix_attention(const void* q, wq_dtype dtype, int64_t q_stride, int64_t B,
                               int64_t Hq, int64_t Hkv, int32_t D, int64_t P, int64_t prefix_cap,
@@ -566,8 +567,9 @@ wq_status wq_workspace_bytes(wq_op op, int64_t M, int64_t N, int64_t K,
  * Test hook for the bounded device waits. The pages have no counterpart: it
  * exists so that the timeout path can be exercised without a device fault.
  * It applies to every later launch, in this process, of the kernels with
- * bounded waits (the tensor-core kernels of wq_w4a16_gemm, of wq_mx_gemm, and
- * of wq_msd_gemm for M > 16):
+ * bounded waits (the tensor-core kernels of wq_w4a16_gemm, of wq_mx_gemm, of
+ * wq_prefix_attention for more than 16 query rows a KV head, and of wq_msd_gemm
+ * for M > 16):
  *   limit_ns  how long any one device wait may last before the kernel gives
  *             up; 0 restores the default of 2 s;
  *   stall     1: the kernel's loader withholds the first k-tile, so the first

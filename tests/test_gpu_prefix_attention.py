@@ -284,3 +284,24 @@ def test_refusals(wq):
     with pytest.raises(wq.WqError):                      # 9 heads over 2
         wq.wq_prefix_attention(torch.zeros(b, 9, D, dtype=torch.bfloat16, device="cuda"), pk, pv, k,
                                v, ln)
+
+
+@pytest.mark.parametrize("b", [8, 40])
+def test_bounded_wait_expires_cleanly(wq, b):
+    """With the first key tile withheld the tensor-core kernel gives up, reports
+    the wait and returns; the next call is right."""
+    hq, hkv, cap, p = 8, 1, 16, 700
+    pk, pv, hpk, hpv = _cache(wq, 1, hkv, p, 30)
+    k, v, hk, hv = _cache(wq, b, hkv, cap, 31)
+    q = torch.randn(b, hq, D, generator=torch.Generator().manual_seed(32)).bfloat16().cuda()
+    ln = _i32([cap] * b)
+    torch.cuda.synchronize()
+    wq.wq_test_set_wait(1_000_000, 1)
+    try:
+        wq.wq_prefix_attention(q, pk, pv, k, v, ln)
+        st, detail = wq.wq_device_error()
+    finally:
+        wq.wq_test_set_wait()
+    assert st == wq.WQ_ERR_TIMEOUT and detail >> 8 in (0x41, 0x42, 0x43)
+    assert wq.wq_device_error()[0] == wq.WQ_OK
+    _check(wq.wq_prefix_attention(q, pk, pv, k, v, ln), q, hpk, hpv, hk, hv, [cap] * b, p)
