@@ -12,8 +12,7 @@
 // Tensor memory holds both streams' scores (128 columns each, overwritten by
 // their fp16 weights) and outputs. Per stream and tile:
 //   S = Q K^T      A, B in shared memory (fp16, 128-byte swizzle, K-major)
-//   softmax        thread = row: the scores are read twice, for the bound and
-//                  for the weights
+//   softmax        a warp takes 32 rows
 //   O += P V       A = the weights in tensor memory
 // Roles: warps 0-3 and 4-7 softmax of stream 0 and 1, warps 8-11 dequantize
 // keys and values into shared memory (two stages each), warp 12 issues.
@@ -75,15 +74,36 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   return r;
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  const uint32_t* v = r;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t t[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = v[16 * h + i];
-    sm100::tmem_st16(taddr + 16 * h, t);
-  }
+// 32 columns of 16 TMEM lanes: registers 4 j .. 4 j + 3 hold columns 8 j +
+// 2 t4, + 1 of row g, then of row g + 8 (lane = 4 g + t4).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 32 columns of 16 lanes, one 32-bit column a lane: column 4 j + t4 of row g is
+// lo[j], of row g + 8 hi[j].
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* lo,
+                                                   const uint32_t* hi) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(lo[0]), "r"(hi[0]), "r"(lo[1]), "r"(hi[1]), "r"(lo[2]), "r"(hi[2]), "r"(lo[3]),
+      "r"(hi[3]), "r"(lo[4]), "r"(hi[4]), "r"(lo[5]), "r"(hi[5]), "r"(lo[6]), "r"(hi[6]),
+      "r"(lo[7]), "r"(hi[7])
+      : "memory");
 }
 
 template <int MT>
@@ -95,7 +115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = smem;                          // [row tile]
   uint8_t* sk = sq + MT * kOpBytes;            // [stage]
   uint8_t* sv = sk + 2 * kOpBytes;             // [stage]
-  float* tab = reinterpret_cast<float*>(sv + 2 * kOpBytes);  // [stage][sk, log2 sv, 1 / sv][128]
+  // [stage] per column pair (sk, sk, log2 sv, log2 sv), then 1 / sv per column
+  float* tab = reinterpret_cast<float*>(sv + 2 * kOpBytes);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tab + kTabs * 3 * kTile);
   uint64_t* q_full = bars;
   uint64_t* k_full = bars + 1;    // [2]
@@ -153,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < 8) {
-    // ---------------- softmax: thread = row ----------------
+    // ---------------- softmax: warp = 32 rows ----------------
     const int s = warp >> 2, q = warp & 3;
     const int r = 32 * q + lane;
     const int row = (MT == 2 ? 2 * rg + s : rg) * kTile + r;
@@ -207,81 +228,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint32_t ts = tmem + lanes + (uint32_t)(s * kTile);
     const uint32_t to = tmem + lanes + (uint32_t)(kColO + s * kD);
-    const uint64_t cr2 = f2(cr, cr);
-    float m = kNone;
-    uint64_t E2 = 0;  // two partial sums: even and odd columns
+    // Scores come in the layout of 16-lane, 8-column accumulator fragments:
+    // lane (g, t4) holds columns 8 j + 2 t4 and + 1 of rows 8 n + g, n = 0 .. 3.
+    // A thread meets a quarter of the columns and takes their table entries for
+    // 4 rows at once: read by one row a thread, 12 bytes a column and lane
+    // filled the shared-memory pipe twice as long as the MMAs run.
+    const int g = lane >> 2, t4 = lane & 3;
+    uint64_t cr2[4], E2[4];
+    float m[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float c = __shfl_sync(0xffffffffu, cr, 8 * n + g);
+      cr2[n] = f2(c, c);
+      E2[n] = 0;
+      m[n] = kNone;
+    }
     bool ok = true;
     int i = 0;
     for (int tile = MT == 2 ? 0 : s; tile < T; tile += MT == 2 ? 1 : 2, ++i) {
       ok = wait(&s_full[s], (uint32_t)i, 0x4101u);
       if (!ok) break;
       sm100::tc_fence_after();
-      const float* tb = tab + (tile % kTabs) * 3 * kTile;
-      // the bound
-      float mx = kNone;
+      const float* tb = tab + (tile % kTabs) * 3 * kTile + 4 * t4;
+      const float* rb = tab + (tile % kTabs) * 3 * kTile + 2 * kTile + 2 * t4;
+      // weights against the present bound, kept in registers until the tile's
+      // largest t is known; if that is too far above the bound (always in a
+      // row's first tile, rarely later) the bound moves and they are computed
+      // again from the scores, which are still in place
+      uint32_t w[4][kTile / 8];  // [row][8 columns: this lane's pair]
+      float mx[4];
+      uint64_t e2[4];
+      auto weigh = [&]() {
+        uint64_t mm[4];
 #pragma unroll
-      for (int c = 0; c < kTile / 32; ++c) {
-        uint32_t v[32];
-        sm100::tmem_ld32(ts + 32 * c, v);
-        sm100::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(tb + 32 * c + 4 * j);
-          const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(tb + kTile + 32 * c + 4 * j);
-          const float2 x = f2_get(f2_fma(
-              f2_mul(f2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), cr2), a.x, b.x));
-          const float2 y = f2_get(f2_fma(
-              f2_mul(f2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), cr2), a.y,
-              b.y));
-          mx = fmaxf(fmaxf(fmaxf(mx, x.x), x.y), fmaxf(y.x, y.y));
+        for (int n = 0; n < 4; ++n) {
+          mm[n] = f2(-m[n], -m[n]);
+          mx[n] = kNone;
+          e2[n] = 0;
         }
-      }
-      const bool grow = mx > m + kSlack;
-      if (__any_sync(0xffffffffu, grow)) {
-        const float nm = grow ? mx : m;  // a row moves by its own scores only
-        const float f = ex2(m - nm);
-        m = nm;
-        E2 = f2_mul(E2, f2(f, f));
-        if (i > 0) {
 #pragma unroll
-          for (int c = 0; c < kD / 32; ++c) {
-            uint32_t v[32];
-            sm100::tmem_ld32(to + 32 * c, v);
-            sm100::tmem_ld_wait();
+        for (int c = 0; c < kTile / 32; ++c) {
+          uint32_t v[2][16];
+          tmem_ld_16x256b_x4(ts + 32 * c, v[0]);
+          tmem_ld_16x256b_x4(ts + (16u << 16) + 32 * c, v[1]);
+          sm100::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-            tmem_st32(to + 32 * c, v);
+          for (int j = 0; j < 4; ++j) {
+            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(tb + 64 * c + 16 * j);
+            const uint64_t d = *reinterpret_cast<const uint64_t*>(rb + 32 * c + 8 * j);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t* u = v[n >> 1] + 4 * j + 2 * (n & 1);
+              const uint64_t t = f2_fma(
+                  f2_mul(f2(__uint_as_float(u[0]), __uint_as_float(u[1])), cr2[n]), a.x, a.y);
+              const float2 x = f2_get(t);
+              mx[n] = fmaxf(mx[n], fmaxf(x.x, x.y));
+              const float2 y = f2_get(f2_add(t, mm[n]));
+              const float w0 = ex2(y.x), w1 = ex2(y.y);
+              e2[n] = f2_fma(f2(w0, w1), d, e2[n]);
+              w[n][4 * c + j] = pack_f16x2(w0, w1);
+            }
           }
         }
-      }
-      // the weights
-      const uint64_t mm = f2(-m, -m);
+      };
+      weigh();
+      bool grow = false;
 #pragma unroll
-      for (int c = 0; c < kTile / 32; ++c) {
-        uint32_t v[32], w[16];
-        sm100::tmem_ld32(ts + 32 * c, v);
-        sm100::tmem_ld_wait();
+      for (int n = 0; n < 4; ++n) grow |= mx[n] > m[n] + kSlack;
+      if (__any_sync(0xffffffffu, grow)) {
+        float f[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(tb + 32 * c + 4 * j);
-          const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(tb + kTile + 32 * c + 4 * j);
-          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(tb + 2 * kTile + 32 * c + 4 * j);
-          const float2 x = f2_get(f2_add(
-              f2_fma(f2_mul(f2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1])), cr2), a.x,
-                     b.x),
-              mm));
-          const float2 y = f2_get(f2_add(
-              f2_fma(f2_mul(f2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])), cr2),
-                     a.y, b.y),
-              mm));
-          const float e0 = ex2(x.x), e1 = ex2(x.y), e2 = ex2(y.x), e3 = ex2(y.y);
-          E2 = f2_fma(f2(e0, e1), d.x, E2);
-          E2 = f2_fma(f2(e2, e3), d.y, E2);
-          w[2 * j] = pack_f16x2(e0, e1);
-          w[2 * j + 1] = pack_f16x2(e2, e3);
+        for (int n = 0; n < 4; ++n) {
+          mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
+          mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
+          // a row moves by its own scores only
+          const float nm = mx[n] > m[n] + kSlack ? mx[n] : m[n];
+          f[n] = ex2(m[n] - nm);
+          m[n] = nm;
+          E2[n] = f2_mul(E2[n], f2(f[n], f[n]));
         }
-        sm100::tmem_st16(ts + 16 * c, w);  // over columns whose scores were read
+        if (i > 0) {
+#pragma unroll
+          for (int c = 0; c < kD / 32; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[16];
+              tmem_ld_16x256b_x4(to + ((uint32_t)(16 * h) << 16) + 32 * c, v);
+              sm100::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                v[j] = __float_as_uint(__uint_as_float(v[j]) * f[2 * h + ((j >> 1) & 1)]);
+              tmem_st_16x256b_x4(to + ((uint32_t)(16 * h) << 16) + 32 * c, v);
+            }
+        }
+        weigh();
       }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) E2[n] = f2_add(E2[n], e2[n]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          tmem_st_16x128b_x8(ts + ((uint32_t)(16 * h) << 16) + 32 * c, w[2 * h] + 8 * c,
+                             w[2 * h + 1] + 8 * c);
       sm100::tmem_st_wait();
       sm100::tc_fence_before();
       __syncwarp();
@@ -290,14 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm100::mbar_arrive(&t_empty[tile % kTabs]);
       }
     }
-    // ---- the row's partial result
+    // ---- the rows' partial results
     const int nslot = p.nsp + p.nso;
     const int slot = MT == 2 ? split : 2 * split + s;
     if (ok && i > 0) ok = wait(&o_full[s], 0, 0x4102u);
     if (ok) {
       sm100::tc_fence_after();
-      const int64_t at =
-          have ? ((int64_t)(row / p.R) * p.Hq + kh * p.R + row % p.R) * nslot + slot : 0;
+      auto place = [&](int rr) {
+        return ((int64_t)(rr / p.R) * p.Hq + kh * p.R + rr % p.R) * nslot + slot;
+      };
+      const int64_t at = have ? place(row) : 0;
       if (i > 0) {
 #pragma unroll
         for (int c = 0; c < kD / 32; ++c) {
@@ -311,8 +362,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
       }
-      const float2 e = f2_get(E2);
-      if (have) p.stat[at] = make_float2(m, e.x + e.y);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float2 x = f2_get(E2[n]);
+        float e = x.x + x.y;
+        e += __shfl_xor_sync(0xffffffffu, e, 1);
+        e += __shfl_xor_sync(0xffffffffu, e, 2);
+        const int rr = row - lane + 8 * n + g;
+        if (t4 == 0 && rr < p.B * p.R) p.stat[place(rr)] = make_float2(m[n], e);
+      }
     }
   } else if (warp < 12) {
     // ---------------- keys and values to fp16 integers ----------------
@@ -390,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float x = fmaxf(__half2float(__ushort_as_half((unsigned short)cur[2])),
                               5.9604645e-8f);  // fp16's smallest: a scale of 0 has no log
         const float l = __log2f(x);
-        tb[pos] = __half2float(__ushort_as_half((unsigned short)cur[0]));
-        tb[kTile + pos] = in ? l : -INFINITY;
+        tb[4 * (pos >> 1) + (pos & 1)] = __half2float(__ushort_as_half((unsigned short)cur[0]));
+        tb[4 * (pos >> 1) + 2 + (pos & 1)] = in ? l : -INFINITY;
         tb[2 * kTile + pos] = in ? ex2(-l) : 0.0f;
       }
       sm100::fence_proxy_async_smem();
