@@ -41,6 +41,7 @@ constexpr int kThreads = 13 * 32;
 constexpr int kOpBytes = kTile * kD * 2;   // an operand tile: two 64-element atoms of 16 KB
 constexpr int kAtomBytes = kOpBytes / 2;
 constexpr int kTabs = 4;                   // key-table stages
+constexpr uint32_t kHalf = 16u << 16;      // the upper 16 lanes of a warp's quarter of TMEM
 constexpr int kColO = 256;                 // TMEM columns of the outputs (scores: 0 and 128)
 
 template <int MT>
@@ -93,17 +94,20 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 32 columns of 16 lanes, one 32-bit column a lane: column 4 j + t4 of row g is
-// lo[j], of row g + 8 hi[j].
-__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t* lo,
-                                                   const uint32_t* hi) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(lo[0]), "r"(hi[0]), "r"(lo[1]), "r"(hi[1]), "r"(lo[2]), "r"(hi[2]), "r"(lo[3]),
-      "r"(hi[3]), "r"(lo[4]), "r"(hi[4]), "r"(lo[5]), "r"(hi[5]), "r"(lo[6]), "r"(hi[6]),
-      "r"(lo[7]), "r"(hi[7])
-      : "memory");
+// 16 columns of 16 lanes, one 32-bit column a lane: registers 2 j, 2 j + 1 hold
+// column 4 j + t4 of rows g and g + 8.
+__device__ __forceinline__ void tmem_ld_16x128b_x4(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
 }
 
 template <int MT>
@@ -234,14 +238,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 4 rows at once: read by one row a thread, 12 bytes a column and lane
     // filled the shared-memory pipe twice as long as the MMAs run.
     const int g = lane >> 2, t4 = lane & 3;
-    uint64_t cr2[4], E2[4];
-    float m[4];
+    uint64_t cr2[4], E2[4], mm[4];  // row factors, sums of even and odd columns, minus the bounds
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float c = __shfl_sync(0xffffffffu, cr, 8 * n + g);
       cr2[n] = f2(c, c);
       E2[n] = 0;
-      m[n] = kNone;
+      mm[n] = f2(-kNone, -kNone);
     }
     bool ok = true;
     int i = 0;
@@ -251,86 +254,92 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_after();
       const float* tb = tab + (tile % kTabs) * 3 * kTile + 4 * t4;
       const float* rb = tab + (tile % kTabs) * 3 * kTile + 2 * kTile + 2 * t4;
-      // weights against the present bound, kept in registers until the tile's
-      // largest t is known; if that is too far above the bound (always in a
-      // row's first tile, rarely later) the bound moves and they are computed
-      // again from the scores, which are still in place
-      uint32_t w[4][kTile / 8];  // [row][8 columns: this lane's pair]
-      float mx[4];
-      uint64_t e2[4];
-      auto weigh = [&]() {
-        uint64_t mm[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          mm[n] = f2(-m[n], -m[n]);
-          mx[n] = kNone;
-          e2[n] = 0;
+      for (int c = 0; c < kTile / 32; ++c) {
+        uint32_t v[2][16];
+        tmem_ld_16x256b_x4(ts + 32 * c, v[0]);
+        tmem_ld_16x256b_x4(ts + kHalf + 32 * c, v[1]);
+        sm100::tmem_ld_wait();
+        uint64_t t[4][4];  // [row][8 columns: this lane's pair]
+        float mx[4] = {kNone, kNone, kNone, kNone};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(tb + 64 * c + 16 * j);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t* u = v[n >> 1] + 4 * j + 2 * (n & 1);
+            t[n][j] = f2_fma(f2_mul(f2(__uint_as_float(u[0]), __uint_as_float(u[1])), cr2[n]), a.x,
+                             a.y);
+            const float2 x = f2_get(t[n][j]);
+            mx[n] = fmaxf(mx[n], fmaxf(x.x, x.y));
+          }
         }
+        bool grow = false;
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c) {
-          uint32_t v[2][16];
-          tmem_ld_16x256b_x4(ts + 32 * c, v[0]);
-          tmem_ld_16x256b_x4(ts + (16u << 16) + 32 * c, v[1]);
-          sm100::tmem_ld_wait();
+        for (int n = 0; n < 4; ++n) grow |= mx[n] > kSlack - f2_get(mm[n]).x;
+        if (__any_sync(0xffffffffu, grow)) {
+          // a bound moves (in a row's first columns, rarely later): what was
+          // summed against the old one is brought down, the weights of this
+          // tile's columns before these among it
+          float f[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(tb + 64 * c + 16 * j);
-            const uint64_t d = *reinterpret_cast<const uint64_t*>(rb + 32 * c + 8 * j);
+          for (int n = 0; n < 4; ++n) {
+            mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
+            mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
+            const float m = -f2_get(mm[n]).x;
+            // a row moves by its own scores only
+            const float nm = mx[n] > m + kSlack ? mx[n] : m;
+            f[n] = ex2(m - nm);
+            mm[n] = f2(-nm, -nm);
+            E2[n] = f2_mul(E2[n], f2(f[n], f[n]));
+          }
+          if (i > 0) {
+#pragma unroll 1
+            for (int k = 0; k < 2 * (kD / 32); ++k) {
+              const int h = k & 1;
+              uint32_t o[16];
+              tmem_ld_16x256b_x4(to + (h ? kHalf : 0) + 32 * (k >> 1), o);
+              sm100::tmem_ld_wait();
+              const float f0 = h ? f[2] : f[0], f1 = h ? f[3] : f[1];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const uint32_t* u = v[n >> 1] + 4 * j + 2 * (n & 1);
-              const uint64_t t = f2_fma(
-                  f2_mul(f2(__uint_as_float(u[0]), __uint_as_float(u[1])), cr2[n]), a.x, a.y);
-              const float2 x = f2_get(t);
-              mx[n] = fmaxf(mx[n], fmaxf(x.x, x.y));
-              const float2 y = f2_get(f2_add(t, mm[n]));
-              const float w0 = ex2(y.x), w1 = ex2(y.y);
-              e2[n] = f2_fma(f2(w0, w1), d, e2[n]);
-              w[n][4 * c + j] = pack_f16x2(w0, w1);
+              for (int j = 0; j < 16; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * (((j >> 1) & 1) ? f1 : f0));
+              tmem_st_16x256b_x4(to + (h ? kHalf : 0) + 32 * (k >> 1), o);
+            }
+          }
+          if (c > 0) {
+            sm100::tmem_st_wait();
+#pragma unroll 1
+            for (int k = 0; k < 2 * c; ++k) {
+              const int h = k & 1;
+              const uint32_t at = ts + (h ? kHalf : 0) + 16 * (k >> 1);
+              uint32_t o[8];
+              tmem_ld_16x128b_x4(at, o);
+              sm100::tmem_ld_wait();
+              const __half2 f0 = __float2half2_rn(h ? f[2] : f[0]);
+              const __half2 f1 = __float2half2_rn(h ? f[3] : f[1]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] = h2(__hmul2(as_h2(o[j]), (j & 1) ? f1 : f0));
+              tmem_st_16x128b_x4(at, o);
             }
           }
         }
-      };
-      weigh();
-      bool grow = false;
+        uint32_t w[2][8];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) grow |= mx[n] > m[n] + kSlack;
-      if (__any_sync(0xffffffffu, grow)) {
-        float f[4];
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = *reinterpret_cast<const uint64_t*>(rb + 32 * c + 8 * j);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
-          mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
-          // a row moves by its own scores only
-          const float nm = mx[n] > m[n] + kSlack ? mx[n] : m[n];
-          f[n] = ex2(m[n] - nm);
-          m[n] = nm;
-          E2[n] = f2_mul(E2[n], f2(f[n], f[n]));
+          for (int n = 0; n < 4; ++n) {
+            const float2 y = f2_get(f2_add(t[n][j], mm[n]));
+            const float w0 = ex2(y.x), w1 = ex2(y.y);
+            E2[n] = f2_fma(f2(w0, w1), d, E2[n]);
+            w[n >> 1][2 * j + (n & 1)] = pack_f16x2(w0, w1);
+          }
         }
-        if (i > 0) {
-#pragma unroll
-          for (int c = 0; c < kD / 32; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[16];
-              tmem_ld_16x256b_x4(to + ((uint32_t)(16 * h) << 16) + 32 * c, v);
-              sm100::tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                v[j] = __float_as_uint(__uint_as_float(v[j]) * f[2 * h + ((j >> 1) & 1)]);
-              tmem_st_16x256b_x4(to + ((uint32_t)(16 * h) << 16) + 32 * c, v);
-            }
-        }
-        weigh();
+        // over columns whose scores were read
+        tmem_st_16x128b_x4(ts + 16 * c, w[0]);
+        tmem_st_16x128b_x4(ts + kHalf + 16 * c, w[1]);
       }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) E2[n] = f2_add(E2[n], e2[n]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          tmem_st_16x128b_x8(ts + ((uint32_t)(16 * h) << 16) + 32 * c, w[2 * h] + 8 * c,
-                             w[2 * h + 1] + 8 * c);
       sm100::tmem_st_wait();
       sm100::tc_fence_before();
       __syncwarp();
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         e += __shfl_xor_sync(0xffffffffu, e, 1);
         e += __shfl_xor_sync(0xffffffffu, e, 2);
         const int rr = row - lane + 8 * n + g;
-        if (t4 == 0 && rr < p.B * p.R) p.stat[place(rr)] = make_float2(m[n], e);
+        if (t4 == 0 && rr < p.B * p.R) p.stat[place(rr)] = make_float2(-f2_get(mm[n]).x, e);
       }
     }
   } else if (warp < 12) {
