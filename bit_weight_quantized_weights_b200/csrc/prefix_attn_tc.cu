@@ -12,10 +12,17 @@
 // Tensor memory holds both streams' scores (128 columns each, overwritten by
 // their fp16 weights) and outputs. Per stream and tile:
 //   S = Q K^T      A, B in shared memory (fp16, 128-byte swizzle, K-major)
-//   softmax        a warp takes 32 rows
+//   softmax        a warp takes 16 rows
 //   O += P V       A = the weights in tensor memory
-// Roles: warps 0-3 and 4-7 softmax of stream 0 and 1, warps 8-11 dequantize
-// keys and values into shared memory (two stages each), warp 12 issues.
+// Roles: warps 0-7 and 8-15 softmax of stream 0 and 1, warps 16-19 dequantize
+// keys and values into shared memory (two stages each), warp 20 issues (21-23
+// fill its warpgroup).
+// The operands are the dequantized values themselves, (q - z) s rounded once to
+// fp16 (2^-11), up to a power of two common to 32 keys: a score's scale and the
+// exponent's offset are then one multiply-add for two columns. Exact integers
+// with the scales in a table per key (read by every row) took 12 bytes a column
+// and row group from shared memory, beside the MMAs' operands, and two more
+// operations a weight: 380 us against the present time at 128 sequences x 65537.
 // Within a group of 8 dimensions (K) or keys (V) the nibbles of a code word
 // come out as pairs (0, 4), (1, 5), (2, 6), (3, 7): Q's dimensions and the rows
 // of K (hence the columns of S and P) are stored in that order, 0 4 1 5 2 6 3 7.
@@ -37,16 +44,20 @@ namespace {
 using namespace prefix;
 
 constexpr int kTile = 128;                 // keys of a tile, rows of a row tile
-constexpr int kThreads = 13 * 32;
+constexpr int kSoftWarps = 16;             // 8 a stream
+constexpr int kIssueWarp = kSoftWarps + 4;
+constexpr int kThreads = 24 * 32;
+// Registers a thread of each warpgroup: 4 * 72 + 152 + 40 = 6 * 80, what the
+// block is launched with; the dequantization keeps the next tile's codes.
+constexpr int kRegsSoftmax = 72, kRegsDequant = 152, kRegsIssue = 40;
 constexpr int kOpBytes = kTile * kD * 2;   // an operand tile: two 64-element atoms of 16 KB
 constexpr int kAtomBytes = kOpBytes / 2;
 constexpr int kTabs = 4;                   // key-table stages
-constexpr uint32_t kHalf = 16u << 16;      // the upper 16 lanes of a warp's quarter of TMEM
 constexpr int kColO = 256;                 // TMEM columns of the outputs (scores: 0 and 128)
 
 template <int MT>
 constexpr int smem_bytes() {
-  return 1024 + (MT + 4) * kOpBytes + kTabs * 3 * kTile * 4 + 256;
+  return 1024 + (MT + 4) * kOpBytes + kTabs * 4 * 16 + 256;
 }
 
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
@@ -64,15 +75,26 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  return h2(__hmul2(as_h2(a), as_h2(b)));
+}
+
+__device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)(127 + x) << 23); }
+
+// fp16 bits of a lane's scale / 2^x, with x (returned) such that the
+// largest of the warp's scales becomes [2^10, 2^11) (a largest below fp16's
+// normal range counts as 2^-14).
+__device__ __forceinline__ uint32_t norm_scale(uint32_t bits, int& x) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, bits & 0x7FFFu);
+  x = max((int)(top >> 10), 1) - 25;
+  const float s = __half2float(__ushort_as_half((unsigned short)bits)) * pow2(-x);
+  return __half_as_ushort(__float2half_rn(s));
 }
 
 // 32 columns of 16 TMEM lanes: registers 4 j .. 4 j + 3 hold columns 8 j +
@@ -119,9 +141,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = smem;                          // [row tile]
   uint8_t* sk = sq + MT * kOpBytes;            // [stage]
   uint8_t* sv = sk + 2 * kOpBytes;             // [stage]
-  // [stage] per column pair (sk, sk, log2 sv, log2 sv), then 1 / sv per column
-  float* tab = reinterpret_cast<float*>(sv + 2 * kOpBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(tab + kTabs * 3 * kTile);
+  // [stage][32 keys]: 2^x of the keys' scales, y of the values', 2^-y
+  float4* tab = reinterpret_cast<float4*>(sv + 2 * kOpBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tab + kTabs * 4);
   uint64_t* q_full = bars;
   uint64_t* k_full = bars + 1;    // [2]
   uint64_t* k_empty = bars + 3;   // [2]
@@ -148,22 +170,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int T = (end - begin + kTile - 1) / kTile;
 
   if (threadIdx.x == 0) {
-    sm100::mbar_init(q_full, 4 * MT);
+    sm100::mbar_init(q_full, 8 * MT);
     for (int i = 0; i < 2; ++i) {
       sm100::mbar_init(&k_full[i], 4);
       sm100::mbar_init(&k_empty[i], 1);
       sm100::mbar_init(&v_full[i], 4);
       sm100::mbar_init(&v_empty[i], 1);
       sm100::mbar_init(&s_full[i], 1);
-      sm100::mbar_init(&p_full[i], 4);
+      sm100::mbar_init(&p_full[i], 8);
       sm100::mbar_init(&o_full[i], 1);
     }
-    for (int i = 0; i < kTabs; ++i) sm100::mbar_init(&t_empty[i], 4 * MT);
+    for (int i = 0; i < kTabs; ++i) sm100::mbar_init(&t_empty[i], 8 * MT);
     sm100::mbar_init(mma_done, 1);
     *abort_flag = 0;
     sm100::fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     sm100::tmem_alloc(tmem_slot, 512);
     sm100::tmem_relinquish();
   }
@@ -177,16 +199,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     abort_flag, wc.limit_ns));
   };
 
-  if (warp < 8) {
-    // ---------------- softmax: warp = 32 rows ----------------
-    const int s = warp >> 2, q = warp & 3;
-    const int r = 32 * q + lane;
-    const int row = (MT == 2 ? 2 * rg + s : rg) * kTile + r;
-    const bool have = row < p.B * p.R;
-    const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    float up = 1.0f, cr = 0.0f;
+  if (warp < kSoftWarps) {
+    // ---------------- softmax: warp = 16 rows ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int s = warp >> 3;                               // stream
+    const int r0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);  // first row: half a TMEM lane quarter
+    const int base = (MT == 2 ? 2 * rg + s : rg) * kTile + r0;
+    const uint32_t lanes = (uint32_t)r0 << 16;
+    const int nrows = p.B * p.R;
+    float cr;
     {
-      // the row of Q as fp16 times a power of two; rows past the batch are zeros
+      // two lanes a row of Q: fp16 times a power of two; rows past the batch are zeros
+      const int r = r0 + (lane >> 1), part = lane & 1;
+      const int row = base + (lane >> 1);
+      const bool have = row < nrows;
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(p.q) +
           (have ? (int64_t)(row / p.R) * p.q_stride + (int64_t)(kh * p.R + row % p.R) * kD : 0));
@@ -205,23 +231,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      float amax = 0.0f, down;
-#pragma unroll 4
-      for (int j = 0; j < kD / 8; ++j) {
+      float amax = 0.0f, up, down;
+#pragma unroll 2
+      for (int j = 0; j < kD / 16; ++j) {
         float f[8];
-        values(j, f);
+        values(8 * part + j, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
       }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       row_scale(amax, up, down);
       cr = down * kScoreScale;
       if (MT == 2 || s == 0) {
-        uint8_t* dst = sq + s * kOpBytes + r * 128;
-#pragma unroll 4
-        for (int j = 0; j < kD / 8; ++j) {
+        uint8_t* dst = sq + s * kOpBytes + part * kAtomBytes + r * 128;
+#pragma unroll 2
+        for (int j = 0; j < kD / 16; ++j) {
           float f[8];
-          values(j, f);
-          *reinterpret_cast<uint4*>(dst + (j >> 3) * kAtomBytes + (((j & 7) ^ (r & 7)) << 4)) =
+          values(8 * part + j, f);
+          *reinterpret_cast<uint4*>(dst + ((j ^ (r & 7)) << 4)) =
               make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up, f[5] * up),
                          pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up, f[7] * up));
         }
@@ -233,18 +260,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + (uint32_t)(s * kTile);
     const uint32_t to = tmem + lanes + (uint32_t)(kColO + s * kD);
     // Scores come in the layout of 16-lane, 8-column accumulator fragments:
-    // lane (g, t4) holds columns 8 j + 2 t4 and + 1 of rows 8 n + g, n = 0 .. 3.
-    // A thread meets a quarter of the columns and takes their table entries for
-    // 4 rows at once: read by one row a thread, 12 bytes a column and lane
-    // filled the shared-memory pipe twice as long as the MMAs run.
+    // lane (g, t4) holds columns 8 j + 2 t4 and + 1 (tokens 8 j + t4 and + 4) of
+    // rows g and g + 8. Eight warps a stream, 16 rows each, keep the exponentials
+    // busy while others of them wait for their scores or store: four warps of 32
+    // rows took 2850 cycles a tile, 1024 of them exponentials.
     const int g = lane >> 2, t4 = lane & 3;
-    uint64_t cr2[4], E2[4], mm[4];  // row factors, sums of even and odd columns, minus the bounds
+    float crow[2], m[2], E[2];  // row factors, bounds, sums
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float c = __shfl_sync(0xffffffffu, cr, 8 * n + g);
-      cr2[n] = f2(c, c);
-      E2[n] = 0;
-      mm[n] = f2(-kNone, -kNone);
+    for (int n = 0; n < 2; ++n) {
+      crow[n] = __shfl_sync(0xffffffffu, cr, 16 * n + 2 * g);
+      E[n] = 0.0f;
+      m[n] = 0.0f;
     }
     bool ok = true;
     int i = 0;
@@ -252,93 +278,106 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(&s_full[s], (uint32_t)i, 0x4101u);
       if (!ok) break;
       sm100::tc_fence_after();
-      const float* tb = tab + (tile % kTabs) * 3 * kTile + 4 * t4;
-      const float* rb = tab + (tile % kTabs) * 3 * kTile + 2 * kTile + 2 * t4;
+      const int key_left = end - begin - tile * kTile;
+      const float4* tb = tab + (tile % kTabs) * 4;
 #pragma unroll
       for (int c = 0; c < kTile / 32; ++c) {
-        uint32_t v[2][16];
-        tmem_ld_16x256b_x4(ts + 32 * c, v[0]);
-        tmem_ld_16x256b_x4(ts + kHalf + 32 * c, v[1]);
+        uint32_t v[16];
+        tmem_ld_16x256b_x4(ts + 32 * c, v);
+        // 32 keys share the powers of two 2^x (scale of the keys), 2^y (of the
+        // values): t - m = S cr 2^x + (y - m), and E takes 2^(t - m) 2^-y
+        const float4 sc = tb[c];
         sm100::tmem_ld_wait();
-        uint64_t t[4][4];  // [row][8 columns: this lane's pair]
-        float mx[4] = {kNone, kNone, kNone, kNone};
+        uint64_t t[2][4];  // [row][8 columns: this lane's pair]
+        float mx[2] = {kNone, kNone};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(tb + 64 * c + 16 * j);
+        for (int n = 0; n < 2; ++n) {
+          const float cf = crow[n] * sc.x, cm = sc.y - m[n];
+          const uint64_t c2 = f2(cf, cf), m2 = f2(cm, cm);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t* u = v[n >> 1] + 4 * j + 2 * (n & 1);
-            t[n][j] = f2_fma(f2_mul(f2(__uint_as_float(u[0]), __uint_as_float(u[1])), cr2[n]), a.x,
-                             a.y);
+          for (int j = 0; j < 4; ++j)
+            t[n][j] = f2_fma(f2(__uint_as_float(v[4 * j + 2 * n]),
+                                __uint_as_float(v[4 * j + 2 * n + 1])), c2, m2);
+        }
+        if (key_left < kTile) {  // the last tile of the prefix: columns without a key
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = 32 * c + 8 * j + t4;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float2 x = f2_get(t[n][j]);
+              t[n][j] = f2(key < key_left ? x.x : -INFINITY, key + 4 < key_left ? x.y : -INFINITY);
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
             const float2 x = f2_get(t[n][j]);
             mx[n] = fmaxf(mx[n], fmaxf(x.x, x.y));
           }
-        }
-        bool grow = false;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) grow |= mx[n] > kSlack - f2_get(mm[n]).x;
-        if (__any_sync(0xffffffffu, grow)) {
+        // the first columns set the bound, whatever their scores
+        const bool first = i == 0 && c == 0;
+        if (__any_sync(0xffffffffu, first || fmaxf(mx[0], mx[1]) > kSlack)) {
           // a bound moves (in a row's first columns, rarely later): what was
           // summed against the old one is brought down, the weights of this
           // tile's columns before these among it
-          float f[4];
+          float f[2];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int n = 0; n < 2; ++n) {
             mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
             mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
-            const float m = -f2_get(mm[n]).x;
-            // a row moves by its own scores only
-            const float nm = mx[n] > m + kSlack ? mx[n] : m;
-            f[n] = ex2(m - nm);
-            mm[n] = f2(-nm, -nm);
-            E2[n] = f2_mul(E2[n], f2(f[n], f[n]));
+            // a row moves by its own scores only; t is relative to the old bound
+            const float up = first || mx[n] > kSlack ? mx[n] : 0.0f;
+            f[n] = first ? 1.0f : ex2(-up);
+            m[n] += up;
+            E[n] *= f[n];
+            const uint64_t u2 = f2(-up, -up);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[n][j] = f2_add(t[n][j], u2);
           }
           if (i > 0) {
 #pragma unroll 1
-            for (int k = 0; k < 2 * (kD / 32); ++k) {
-              const int h = k & 1;
+            for (int k = 0; k < kD / 32; ++k) {
               uint32_t o[16];
-              tmem_ld_16x256b_x4(to + (h ? kHalf : 0) + 32 * (k >> 1), o);
+              tmem_ld_16x256b_x4(to + 32 * k, o);
               sm100::tmem_ld_wait();
-              const float f0 = h ? f[2] : f[0], f1 = h ? f[3] : f[1];
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                o[j] = __float_as_uint(__uint_as_float(o[j]) * (((j >> 1) & 1) ? f1 : f0));
-              tmem_st_16x256b_x4(to + (h ? kHalf : 0) + 32 * (k >> 1), o);
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
+              tmem_st_16x256b_x4(to + 32 * k, o);
             }
           }
           if (c > 0) {
             sm100::tmem_st_wait();
 #pragma unroll 1
-            for (int k = 0; k < 2 * c; ++k) {
-              const int h = k & 1;
-              const uint32_t at = ts + (h ? kHalf : 0) + 16 * (k >> 1);
+            for (int k = 0; k < c; ++k) {
               uint32_t o[8];
-              tmem_ld_16x128b_x4(at, o);
+              tmem_ld_16x128b_x4(ts + 16 * k, o);
               sm100::tmem_ld_wait();
-              const __half2 f0 = __float2half2_rn(h ? f[2] : f[0]);
-              const __half2 f1 = __float2half2_rn(h ? f[3] : f[1]);
+              const __half2 f0 = __float2half2_rn(f[0]), f1 = __float2half2_rn(f[1]);
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[j] = h2(__hmul2(as_h2(o[j]), (j & 1) ? f1 : f0));
-              tmem_st_16x128b_x4(at, o);
+              tmem_st_16x128b_x4(ts + 16 * k, o);
             }
           }
         }
-        uint32_t w[2][8];
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t d = *reinterpret_cast<const uint64_t*>(rb + 32 * c + 8 * j);
+        for (int n = 0; n < 2; ++n) {
+          uint64_t e2 = 0;
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const float2 y = f2_get(f2_add(t[n][j], mm[n]));
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = f2_get(t[n][j]);
             const float w0 = ex2(y.x), w1 = ex2(y.y);
-            E2[n] = f2_fma(f2(w0, w1), d, E2[n]);
-            w[n >> 1][2 * j + (n & 1)] = pack_f16x2(w0, w1);
+            e2 = f2_add(e2, f2(w0, w1));
+            w[2 * j + n] = pack_f16x2(w0, w1);
           }
+          const float2 e = f2_get(e2);
+          E[n] = fmaf(e.x + e.y, sc.z, E[n]);
         }
-        // over columns whose scores were read
-        tmem_st_16x128b_x4(ts + 16 * c, w[0]);
-        tmem_st_16x128b_x4(ts + kHalf + 16 * c, w[1]);
+        tmem_st_16x128b_x4(ts + 16 * c, w);  // over columns whose scores were read
       }
       sm100::tmem_st_wait();
       sm100::tc_fence_before();
@@ -354,42 +393,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && i > 0) ok = wait(&o_full[s], 0, 0x4102u);
     if (ok) {
       sm100::tc_fence_after();
-      auto place = [&](int rr) {
-        return ((int64_t)(rr / p.R) * p.Hq + kh * p.R + rr % p.R) * nslot + slot;
-      };
-      const int64_t at = have ? place(row) : 0;
+      int64_t at[2];
+      bool have[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int row = base + 8 * n + g;
+        have[n] = row < nrows;
+        at[n] = ((int64_t)(row / p.R) * p.Hq + kh * p.R + row % p.R) * nslot + slot;
+        E[n] += __shfl_xor_sync(0xffffffffu, E[n], 1);
+        E[n] += __shfl_xor_sync(0xffffffffu, E[n], 2);
+        if (t4 == 0 && have[n]) p.stat[at[n]] = make_float2(i > 0 ? m[n] : kNone, E[n]);
+      }
       if (i > 0) {
 #pragma unroll
         for (int c = 0; c < kD / 32; ++c) {
-          uint32_t v[32];
-          sm100::tmem_ld32(to + 32 * c, v);
+          uint32_t v[16];
+          tmem_ld_16x256b_x4(to + 32 * c, v);
           sm100::tmem_ld_wait();
-          if (have)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(p.part + at * kD + 32 * c + 4 * j) =
-                  make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              if (have[n])
+                *reinterpret_cast<uint2*>(p.part + at[n] * kD + 32 * c + 8 * j + 2 * t4) =
+                    make_uint2(v[4 * j + 2 * n], v[4 * j + 2 * n + 1]);
         }
       }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float2 x = f2_get(E2[n]);
-        float e = x.x + x.y;
-        e += __shfl_xor_sync(0xffffffffu, e, 1);
-        e += __shfl_xor_sync(0xffffffffu, e, 2);
-        const int rr = row - lane + 8 * n + g;
-        if (t4 == 0 && rr < p.B * p.R) p.stat[place(rr)] = make_float2(-f2_get(mm[n]).x, e);
-      }
     }
-  } else if (warp < 12) {
-    // ---------------- keys and values to fp16 integers ----------------
-    const int w = warp - 8;
+  } else if (warp < kSoftWarps + 4) {
+    // ---------------- keys and values to fp16 ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
+    const int w = warp - kSoftWarps;
     const int64_t crow = (int64_t)kh * p.pre.cap, vrow = (int64_t)kh * p.pre.nblk;
     // K: lane = 16-byte piece `piece` of token 8 i + kt of the warp's 32
     const int kt = lane >> 2, piece = lane & 3;
     // token t of 8 sits at row ((t & 3) << 1) | (t >> 2)
     const int krow = ((kt & 3) << 1) | (kt >> 2);
-    const int pos = 32 * w + (lane & 24) + (((lane & 3) << 1) | ((lane >> 2) & 1));
     uint4 kr[4];
     uint32_t vr[16];
     uint32_t cur[4], nxt[4];  // fp16 bits of this lane's token: sk, zk, sv, zv
@@ -429,8 +468,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tile >= 2 && !wait(&k_empty[st], use - 1u, 0x4201u)) break;
       if (tile >= kTabs && !wait(&t_empty[tile % kTabs], (uint32_t)(tile / kTabs) - 1u, 0x4202u))
         break;
+      // the 32 keys' scales, K's and V's, times a power of two that brings the
+      // largest to [2^10, 2^11): a product with q - z is at most 30705, and stays
+      // a normal fp16 number down to scales 2^-24 of the largest
+      int kx, vx;
+      const uint32_t ks = norm_scale(cur[0], kx), vs = norm_scale(cur[2], vx);
+      if (lane == 0)
+        tab[(tile % kTabs) * 4 + w] = make_float4(pow2(kx), (float)vx, pow2(-vx), 0.0f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const uint32_t s2 = __shfl_sync(0xffffffffu, ks, 8 * i + kt) * 0x10001u;
         const uint32_t z = __shfl_sync(0xffffffffu, cur[1], 8 * i + kt) * 0x10001u;
         const uint32_t z1 = h2(__hadd2(as_h2(z), as_h2(0x64006400u)));
         const uint32_t z64 = h2(__hneg2(__hadd2(as_h2(z), as_h2(0x54005400u))));
@@ -446,33 +493,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t a0, a1, a2, a3;
           codes_f16(u[j], z1, z64, a0, a1);
           codes_f16(u[j] >> 8, z1, z64, a2, a3);
+          a0 = mul_f16x2(a0, s2), a1 = mul_f16x2(a1, s2);
+          a2 = mul_f16x2(a2, s2), a3 = mul_f16x2(a3, s2);
           const int chunk = 4 * (piece & 1) + (j ^ (sw ? 1 : 0));
           *reinterpret_cast<uint4*>(dst + ((chunk ^ (row & 7)) << 4)) = make_uint4(a0, a1, a2, a3);
         }
-      }
-      {
-        // per key: sk, log2 sv, 1 / sv; keys past the end weigh 2^-inf
-        const bool in = begin + tile * kTile + 32 * w + lane < end;
-        float* tb = tab + (tile % kTabs) * 3 * kTile;
-        const float x = fmaxf(__half2float(__ushort_as_half((unsigned short)cur[2])),
-                              5.9604645e-8f);  // fp16's smallest: a scale of 0 has no log
-        const float l = __log2f(x);
-        tb[4 * (pos >> 1) + (pos & 1)] = __half2float(__ushort_as_half((unsigned short)cur[0]));
-        tb[4 * (pos >> 1) + 2 + (pos & 1)] = in ? l : -INFINITY;
-        tb[2 * kTile + pos] = in ? ex2(-l) : 0.0f;
       }
       sm100::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && !(wc.stall && tile == 0)) sm100::mbar_arrive(&k_full[st]);
       if (tile + 1 < T) load_k(tile + 1, nxt);
       if (tile >= 2 && !wait(&v_empty[st], use - 1u, 0x4203u)) break;
-      // zeros of 8 tokens as the pairs (0, 4), (1, 5), (2, 6), (3, 7): lane
-      // 8 j + t holds pair t of block j
+      // zeros and scales of 8 tokens as the pairs (0, 4), (1, 5), (2, 6), (3, 7):
+      // lane 8 j + t holds pair t of block j
       const uint32_t zp =
           prmt(cur[3], __shfl_down_sync(0xffffffffu, cur[3], 4), 0x5410);
+      const uint32_t sp = prmt(vs, __shfl_down_sync(0xffffffffu, vs, 4), 0x5410);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t y1[2], y64[2];
+        uint32_t y1[2], y64[2], s2[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) s2[t] = __shfl_sync(0xffffffffu, sp, 8 * j + t);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           y1[t] = h2(__hadd2(as_h2(__shfl_sync(0xffffffffu, zp, 8 * j + 2 * t)),
@@ -487,6 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t a0, a1, a2, a3;
           codes_f16(vr[4 * j + i], y1[0], y64[0], a0, a1);
           codes_f16(vr[4 * j + i] >> 8, y1[1], y64[1], a2, a3);
+          a0 = mul_f16x2(a0, s2[0]), a1 = mul_f16x2(a1, s2[1]);
+          a2 = mul_f16x2(a2, s2[2]), a3 = mul_f16x2(a3, s2[3]);
           *reinterpret_cast<uint4*>(sv + st * kOpBytes + (w >> 1) * kAtomBytes + d * 128 +
                                     ((chunk ^ (d & 7)) << 4)) = make_uint4(a0, a1, a2, a3);
         }
@@ -499,6 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+  }
+  if (warp == kIssueWarp) {
     // ---------------- MMA issue ----------------
     constexpr uint32_t idesc = sm100::idesc_f16_f32(kTile, kTile);
     const uint32_t tm = sm100::uniform(tmem);
@@ -583,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   sm100::tc_fence_after();
-  if (warp == 12) sm100::tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) sm100::tmem_dealloc(tmem, 512);
 }
 
 template <int MT>
