@@ -14,9 +14,9 @@
 //   S = Q K^T      A, B in shared memory (fp16, 128-byte swizzle, K-major)
 //   softmax        a warp takes 16 rows
 //   O += P V       A = the weights in tensor memory
-// Roles: warps 0-7 and 8-15 softmax of stream 0 and 1, warps 16-19 dequantize
-// keys and values into shared memory (two stages each), warp 20 issues (21-23
-// fill its warpgroup).
+// Roles: warps 0-7 and 8-15 softmax of stream 0 and 1, warps 16-23 dequantize
+// keys and values into shared memory (two stages each; 16 keys a warp), warp 24
+// issues (25-27 fill its warpgroup).
 // The operands are the dequantized values themselves, (q - z) s rounded once to
 // fp16 (2^-11), up to a power of two common to 32 keys: a score's scale and the
 // exponent's offset are then one multiply-add for two columns. Exact integers
@@ -45,11 +45,12 @@ using namespace prefix;
 
 constexpr int kTile = 128;                 // keys of a tile, rows of a row tile
 constexpr int kSoftWarps = 16;             // 8 a stream
-constexpr int kIssueWarp = kSoftWarps + 4;
-constexpr int kThreads = 24 * 32;
-// Registers a thread of each warpgroup: 4 * 72 + 152 + 40 = 6 * 80, what the
+constexpr int kDeqWarps = 8;
+constexpr int kIssueWarp = kSoftWarps + kDeqWarps;
+constexpr int kThreads = 28 * 32;
+// Registers a thread of each warpgroup (72 the softmax): 4 * 72 + 2 * 88 + 40 = 7 * 72, what the
 // block is launched with; the dequantization keeps the next tile's codes.
-constexpr int kRegsSoftmax = 72, kRegsDequant = 152, kRegsIssue = 40;
+constexpr int kRegsDequant = 88, kRegsIssue = 40;
 constexpr int kOpBytes = kTile * kD * 2;   // an operand tile: two 64-element atoms of 16 KB
 constexpr int kAtomBytes = kOpBytes / 2;
 constexpr int kTabs = 4;                   // key-table stages
@@ -172,9 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     sm100::mbar_init(q_full, 8 * MT);
     for (int i = 0; i < 2; ++i) {
-      sm100::mbar_init(&k_full[i], 4);
+      sm100::mbar_init(&k_full[i], kDeqWarps);
       sm100::mbar_init(&k_empty[i], 1);
-      sm100::mbar_init(&v_full[i], 4);
+      sm100::mbar_init(&v_full[i], kDeqWarps);
       sm100::mbar_init(&v_empty[i], 1);
       sm100::mbar_init(&s_full[i], 1);
       sm100::mbar_init(&p_full[i], 8);
@@ -201,7 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSoftWarps) {
     // ---------------- softmax: warp = 16 rows ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int s = warp >> 3;                               // stream
     const int r0 = 32 * (warp & 3) + 16 * ((warp >> 2) & 1);  // first row: half a TMEM lane quarter
     const int base = (MT == 2 ? 2 * rg + s : rg) * kTile + r0;
@@ -420,23 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < kSoftWarps + 4) {
+  } else if (warp < kSoftWarps + kDeqWarps) {
     // ---------------- keys and values to fp16 ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
-    const int w = warp - kSoftWarps;
+    const int w = (warp - kSoftWarps) >> 1;       // group of 32 keys
+    const int half = (warp - kSoftWarps) & 1;     // of its 16-key halves, this warp's
     const int64_t crow = (int64_t)kh * p.pre.cap, vrow = (int64_t)kh * p.pre.nblk;
-    // K: lane = 16-byte piece `piece` of token 8 i + kt of the warp's 32
+    // K: lane = 16-byte piece `piece` of token 8 i + kt of the warp's 16
     const int kt = lane >> 2, piece = lane & 3;
     // token t of 8 sits at row ((t & 3) << 1) | (t >> 2)
     const int krow = ((kt & 3) << 1) | (kt >> 2);
-    uint4 kr[4];
-    uint32_t vr[16];
-    uint32_t cur[4], nxt[4];  // fp16 bits of this lane's token: sk, zk, sv, zv
+    uint4 kr[2];
+    uint32_t vr[8];
+    uint32_t cur[4], nxt[4];  // fp16 bits of the group's token `lane`: sk, zk, sv, zv
     auto load_k = [&](int tile, uint32_t (&sc)[4]) {
       const int key0 = begin + tile * kTile + 32 * w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = key0 + 8 * i + kt;
+      for (int i = 0; i < 2; ++i) {
+        const int key = key0 + 16 * half + 8 * i + kt;
         kr[i] = key < end ? ld_stream_u4(p.pre.kc + (crow + key) * (kD / 8) + 4 * piece)
                           : make_uint4(0, 0, 0, 0);
       }
@@ -448,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         sc[i] = in ? reinterpret_cast<const uint16_t*>(t[i])[crow + key] : 0u;
     };
     auto load_v = [&](int tile) {
-      const int blk0 = (begin + tile * kTile) / 8 + 4 * w;
+      const int blk0 = (begin + tile * kTile) / 8 + 4 * w + 2 * half;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           vr[4 * j + i] =
@@ -473,15 +474,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a normal fp16 number down to scales 2^-24 of the largest
       int kx, vx;
       const uint32_t ks = norm_scale(cur[0], kx), vs = norm_scale(cur[2], vx);
-      if (lane == 0)
+      if (lane == 0 && half == 0)
         tab[(tile % kTabs) * 4 + w] = make_float4(pow2(kx), (float)vx, pow2(-vx), 0.0f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t s2 = __shfl_sync(0xffffffffu, ks, 8 * i + kt) * 0x10001u;
-        const uint32_t z = __shfl_sync(0xffffffffu, cur[1], 8 * i + kt) * 0x10001u;
+      for (int i = 0; i < 2; ++i) {
+        const int token = 16 * half + 8 * i + kt;
+        const uint32_t s2 = __shfl_sync(0xffffffffu, ks, token) * 0x10001u;
+        const uint32_t z = __shfl_sync(0xffffffffu, cur[1], token) * 0x10001u;
         const uint32_t z1 = h2(__hadd2(as_h2(z), as_h2(0x64006400u)));
         const uint32_t z64 = h2(__hneg2(__hadd2(as_h2(z), as_h2(0x54005400u))));
-        const int row = 32 * w + 8 * i + krow;
+        const int row = 32 * w + 16 * half + 8 * i + krow;
         uint8_t* dst = sk + st * kOpBytes + (piece >> 1) * kAtomBytes + row * 128;
         // pieces of the second 64 dimensions take their words in the order
         // 1 0 3 2: the 8 lanes of a store phase then hit distinct banks
@@ -510,18 +512,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           prmt(cur[3], __shfl_down_sync(0xffffffffu, cur[3], 4), 0x5410);
       const uint32_t sp = prmt(vs, __shfl_down_sync(0xffffffffu, vs, 4), 0x5410);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 2; ++j) {
+        const int b = 2 * half + j;  // block of the group
         uint32_t y1[2], y64[2], s2[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) s2[t] = __shfl_sync(0xffffffffu, sp, 8 * j + t);
+        for (int t = 0; t < 4; ++t) s2[t] = __shfl_sync(0xffffffffu, sp, 8 * b + t);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          y1[t] = h2(__hadd2(as_h2(__shfl_sync(0xffffffffu, zp, 8 * j + 2 * t)),
+          y1[t] = h2(__hadd2(as_h2(__shfl_sync(0xffffffffu, zp, 8 * b + 2 * t)),
                              as_h2(0x64006400u)));
-          y64[t] = h2(__hneg2(__hadd2(as_h2(__shfl_sync(0xffffffffu, zp, 8 * j + 2 * t + 1)),
+          y64[t] = h2(__hneg2(__hadd2(as_h2(__shfl_sync(0xffffffffu, zp, 8 * b + 2 * t + 1)),
                                       as_h2(0x54005400u))));
         }
-        const int chunk = 4 * (w & 1) + j;
+        const int chunk = 4 * (w & 1) + b;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int d = 32 * i + lane;
