@@ -53,6 +53,7 @@ constexpr int kThreads = 28 * 32;
 constexpr int kRegsDequant = 88, kRegsIssue = 40;
 constexpr int kOpBytes = kTile * kD * 2;   // an operand tile: two 64-element atoms of 16 KB
 constexpr int kAtomBytes = kOpBytes / 2;
+constexpr float kSumMax = 2048.0f;         // of a lane's 4 weights, before a bound moves
 constexpr int kTabs = 4;                   // key-table stages
 constexpr int kColO = 256;                 // TMEM columns of the outputs (scores: 0 and 128)
 
@@ -74,6 +75,11 @@ __device__ __forceinline__ float2 f2_get(uint64_t v) {
 __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
@@ -109,13 +115,18 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
 }
 // 16 columns of 16 lanes, one 32-bit column a lane: registers 2 j, 2 j + 1 hold
 // column 4 j + t4 of rows g and g + 8.
@@ -196,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    return __all_sync(0xffffffffu, sm100::mbar_wait(bar, parity & 1u, &g_prefix_error, site,
-                                                    abort_flag, wc.limit_ns));
+    return __all_sync(0xffffffffu, sm100::mbar_wait_hint(bar, parity & 1u, &g_prefix_error, site,
+                                                         abort_flag, wc.limit_ns, 1000));
   };
 
   if (warp < kSoftWarps) {
@@ -265,11 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // busy while others of them wait for their scores or store: four warps of 32
     // rows took 2850 cycles a tile, 1024 of them exponentials.
     const int g = lane >> 2, t4 = lane & 3;
-    float crow[2], m[2], E[2];  // row factors, bounds, sums
+    float crow[2], m[2];  // row factors, bounds
+    uint64_t E2[2];       // sums of even and odd columns
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       crow[n] = __shfl_sync(0xffffffffu, cr, 16 * n + 2 * g);
-      E[n] = 0.0f;
+      E2[n] = 0;
       m[n] = 0.0f;
     }
     bool ok = true;
@@ -280,16 +292,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_after();
       const int key_left = end - begin - tile * kTile;
       const float4* tb = tab + (tile % kTabs) * 4;
+      uint32_t v[16];
+      tmem_ld_16x256b_x4(ts, v);
 #pragma unroll
       for (int c = 0; c < kTile / 32; ++c) {
-        uint32_t v[16];
-        tmem_ld_16x256b_x4(ts + 32 * c, v);
         // 32 keys share the powers of two 2^x (scale of the keys), 2^y (of the
         // values): t - m = S cr 2^x + (y - m), and E takes 2^(t - m) 2^-y
         const float4 sc = tb[c];
-        sm100::tmem_ld_wait();
         uint64_t t[2][4];  // [row][8 columns: this lane's pair]
-        float mx[2] = {kNone, kNone};
+        sm100::tmem_ld_wait();
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const float cf = crow[n] * sc.x, cm = sc.y - m[n];
@@ -299,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             t[n][j] = f2_fma(f2(__uint_as_float(v[4 * j + 2 * n]),
                                 __uint_as_float(v[4 * j + 2 * n + 1])), c2, m2);
         }
+        if (c + 1 < kTile / 32) tmem_ld_16x256b_x4(ts + 32 * (c + 1), v);
         if (key_left < kTile) {  // the last tile of the prefix: columns without a key
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -310,43 +322,64 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        uint32_t w[8];
+        uint64_t e2[2];
+        auto weigh = [&]() {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x = f2_get(t[n][j]);
-            mx[n] = fmaxf(mx[n], fmaxf(x.x, x.y));
-          }
-        // the first columns set the bound, whatever their scores
+            for (int j = 0; j < 4; ++j) {
+              const float2 y = f2_get(t[n][j]);
+              const float w0 = ex2(y.x), w1 = ex2(y.y);
+              e2[n] = j == 0 ? f2(w0, w1) : f2_add(e2[n], f2(w0, w1));
+              w[2 * j + n] = pack_f16x2(w0, w1);
+            }
+        };
+        weigh();
+        // No weight is above a lane's sums of 4: while those stay below 2^11 they
+        // all fit fp16, and no maximum is needed. The first columns set the
+        // bound, whatever their scores.
         const bool first = i == 0 && c == 0;
-        if (__any_sync(0xffffffffu, first || fmaxf(mx[0], mx[1]) > kSlack)) {
+        const float2 e0 = f2_get(e2[0]), e1 = f2_get(e2[1]);
+        if (__any_sync(0xffffffffu,
+                       first || fmaxf(fmaxf(e0.x, e0.y), fmaxf(e1.x, e1.y)) > kSumMax)) {
           // a bound moves (in a row's first columns, rarely later): what was
           // summed against the old one is brought down, the weights of this
           // tile's columns before these among it
           float f[2];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
-            mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
+            const float2 e = f2_get(e2[n]);
+            float mx = kNone, sum = fmaxf(e.x, e.y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 x = f2_get(t[n][j]);
+              mx = fmaxf(mx, fmaxf(x.x, x.y));
+            }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+            }
             // a row moves by its own scores only; t is relative to the old bound
-            const float up = first || mx[n] > kSlack ? mx[n] : 0.0f;
+            const float up = first || sum > kSumMax ? mx : 0.0f;
             f[n] = first ? 1.0f : ex2(-up);
             m[n] += up;
-            E[n] *= f[n];
+            E2[n] = f2_mul(E2[n], f2(f[n], f[n]));
             const uint64_t u2 = f2(-up, -up);
 #pragma unroll
             for (int j = 0; j < 4; ++j) t[n][j] = f2_add(t[n][j], u2);
           }
           if (i > 0) {
 #pragma unroll 1
-            for (int k = 0; k < kD / 32; ++k) {
-              uint32_t o[16];
-              tmem_ld_16x256b_x4(to + 32 * k, o);
+            for (int k = 0; k < kD / 16; ++k) {
+              uint32_t o[8];
+              tmem_ld_16x256b_x2(to + 16 * k, o);
               sm100::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
+              for (int j = 0; j < 8; ++j)
                 o[j] = __float_as_uint(__uint_as_float(o[j]) * f[(j >> 1) & 1]);
-              tmem_st_16x256b_x4(to + 32 * k, o);
+              tmem_st_16x256b_x2(to + 16 * k, o);
             }
           }
           if (c > 0) {
@@ -362,21 +395,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_16x128b_x4(ts + 16 * k, o);
             }
           }
+          weigh();
         }
-        uint32_t w[8];
+        const uint64_t z2 = f2(sc.z, sc.z);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint64_t e2 = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = f2_get(t[n][j]);
-            const float w0 = ex2(y.x), w1 = ex2(y.y);
-            e2 = f2_add(e2, f2(w0, w1));
-            w[2 * j + n] = pack_f16x2(w0, w1);
-          }
-          const float2 e = f2_get(e2);
-          E[n] = fmaf(e.x + e.y, sc.z, E[n]);
-        }
+        for (int n = 0; n < 2; ++n) E2[n] = f2_fma(e2[n], z2, E2[n]);
         tmem_st_16x128b_x4(ts + 16 * c, w);  // over columns whose scores were read
       }
       sm100::tmem_st_wait();
@@ -400,9 +423,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = base + 8 * n + g;
         have[n] = row < nrows;
         at[n] = ((int64_t)(row / p.R) * p.Hq + kh * p.R + row % p.R) * nslot + slot;
-        E[n] += __shfl_xor_sync(0xffffffffu, E[n], 1);
-        E[n] += __shfl_xor_sync(0xffffffffu, E[n], 2);
-        if (t4 == 0 && have[n]) p.stat[at[n]] = make_float2(i > 0 ? m[n] : kNone, E[n]);
+        const float2 e2 = f2_get(E2[n]);
+        float e = e2.x + e2.y;
+        e += __shfl_xor_sync(0xffffffffu, e, 1);
+        e += __shfl_xor_sync(0xffffffffu, e, 2);
+        if (t4 == 0 && have[n]) p.stat[at[n]] = make_float2(i > 0 ? m[n] : kNone, e);
       }
       if (i > 0) {
 #pragma unroll
@@ -433,35 +458,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint4 kr[2];
     uint32_t vr[8];
     uint32_t cur[4], nxt[4];  // fp16 bits of the group's token `lane`: sk, zk, sv, zv
-    auto load_k = [&](int tile, uint32_t (&sc)[4]) {
-      const int key0 = begin + tile * kTile + 32 * w;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = key0 + 16 * half + 8 * i + kt;
-        kr[i] = key < end ? ld_stream_u4(p.pre.kc + (crow + key) * (kD / 8) + 4 * piece)
-                          : make_uint4(0, 0, 0, 0);
-      }
-      const int key = key0 + lane;
-      const bool in = key < end;
+    // running pointers to this lane's pieces of the tile
+    const int key0 = begin + 32 * w;
+    const uint32_t* kp = p.pre.kc + (crow + key0 + 16 * half + kt) * (kD / 8) + 4 * piece;
+    const uint32_t* vp = p.pre.vc + (vrow + key0 / 8 + 2 * half) * kD + lane;
+    const uint16_t* sp4[4];
+    {
       const __half* t[4] = {p.pre.ks, p.pre.kz, p.pre.vs, p.pre.vz};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        sc[i] = in ? reinterpret_cast<const uint16_t*>(t[i])[crow + key] : 0u;
-    };
-    auto load_v = [&](int tile) {
-      const int blk0 = (begin + tile * kTile) / 8 + 4 * w + 2 * half;
+        sp4[i] = reinterpret_cast<const uint16_t*>(t[i]) + crow + key0 + lane;
+    }
+    int left_k = end - key0, left_v = left_k;  // keys from the group's first on
+    auto load_k = [&](uint32_t (&sc)[4]) {
+      if (left_k >= 32) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int i = 0; i < 2; ++i) kr[i] = ld_stream_u4(kp + 8 * i * (kD / 8));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vr[4 * j + i] =
-              8 * (blk0 + j) < end
-                  ? __ldg(p.pre.vc + (vrow + blk0 + j) * kD + 32 * i + lane)
-                  : 0u;
+        for (int i = 0; i < 4; ++i) sc[i] = *sp4[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          kr[i] = 16 * half + 8 * i + kt < left_k ? ld_stream_u4(kp + 8 * i * (kD / 8))
+                                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[i] = lane < left_k ? *sp4[i] : 0u;
+      }
+      kp += kTile * (kD / 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sp4[i] += kTile;
+      left_k -= kTile;
     };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool in = 16 * half + 8 * j < left_v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[4 * j + i] = in ? __ldg(vp + j * kD + 32 * i) : 0u;
+      }
+      vp += kTile / 8 * kD;
+      left_v -= kTile;
+    };
+    // where this lane's 16-byte pieces go: K's word j of a row (words of the
+    // second 64 dimensions in the order 1 0 3 2, so that the 8 lanes of a store
+    // phase hit distinct banks), V's block j (row d = 32 i + lane)
+    const bool sw = piece >= 2;
+    uint32_t koff[4], voff[2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      koff[j] = (uint32_t)((piece >> 1) * kAtomBytes + (32 * w + 16 * half + krow) * 128 +
+                           (((4 * (piece & 1) + (j ^ (sw ? 1 : 0))) ^ krow) << 4));
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      voff[j] = (uint32_t)((w >> 1) * kAtomBytes + lane * 128 +
+                           (((4 * (w & 1) + 2 * half + j) ^ (lane & 7)) << 4));
     if (T > 0) {
-      load_k(0, cur);
-      load_v(0);
+      load_k(cur);
+      load_v();
     }
     for (int tile = 0; tile < T; ++tile) {
       const int st = tile & 1;
@@ -483,11 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t z = __shfl_sync(0xffffffffu, cur[1], token) * 0x10001u;
         const uint32_t z1 = h2(__hadd2(as_h2(z), as_h2(0x64006400u)));
         const uint32_t z64 = h2(__hneg2(__hadd2(as_h2(z), as_h2(0x54005400u))));
-        const int row = 32 * w + 16 * half + 8 * i + krow;
-        uint8_t* dst = sk + st * kOpBytes + (piece >> 1) * kAtomBytes + row * 128;
-        // pieces of the second 64 dimensions take their words in the order
-        // 1 0 3 2: the 8 lanes of a store phase then hit distinct banks
-        const bool sw = piece >= 2;
+        uint8_t* dst = sk + st * kOpBytes + 8 * i * 128;
         const uint32_t u[4] = {sw ? kr[i].y : kr[i].x, sw ? kr[i].x : kr[i].y,
                                sw ? kr[i].w : kr[i].z, sw ? kr[i].z : kr[i].w};
 #pragma unroll
@@ -497,14 +546,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           codes_f16(u[j] >> 8, z1, z64, a2, a3);
           a0 = mul_f16x2(a0, s2), a1 = mul_f16x2(a1, s2);
           a2 = mul_f16x2(a2, s2), a3 = mul_f16x2(a3, s2);
-          const int chunk = 4 * (piece & 1) + (j ^ (sw ? 1 : 0));
-          *reinterpret_cast<uint4*>(dst + ((chunk ^ (row & 7)) << 4)) = make_uint4(a0, a1, a2, a3);
+          *reinterpret_cast<uint4*>(dst + koff[j]) = make_uint4(a0, a1, a2, a3);
         }
       }
       sm100::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && !(wc.stall && tile == 0)) sm100::mbar_arrive(&k_full[st]);
-      if (tile + 1 < T) load_k(tile + 1, nxt);
+      if (tile + 1 < T) load_k(nxt);
       if (tile >= 2 && !wait(&v_empty[st], use - 1u, 0x4203u)) break;
       // zeros and scales of 8 tokens as the pairs (0, 4), (1, 5), (2, 6), (3, 7):
       // lane 8 j + t holds pair t of block j
@@ -524,23 +572,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           y64[t] = h2(__hneg2(__hadd2(as_h2(__shfl_sync(0xffffffffu, zp, 8 * b + 2 * t + 1)),
                                       as_h2(0x54005400u))));
         }
-        const int chunk = 4 * (w & 1) + b;
+        uint8_t* dst = sv + st * kOpBytes + voff[j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int d = 32 * i + lane;
           uint32_t a0, a1, a2, a3;
           codes_f16(vr[4 * j + i], y1[0], y64[0], a0, a1);
           codes_f16(vr[4 * j + i] >> 8, y1[1], y64[1], a2, a3);
           a0 = mul_f16x2(a0, s2[0]), a1 = mul_f16x2(a1, s2[1]);
           a2 = mul_f16x2(a2, s2[2]), a3 = mul_f16x2(a3, s2[3]);
-          *reinterpret_cast<uint4*>(sv + st * kOpBytes + (w >> 1) * kAtomBytes + d * 128 +
-                                    ((chunk ^ (d & 7)) << 4)) = make_uint4(a0, a1, a2, a3);
+          *reinterpret_cast<uint4*>(dst + 32 * i * 128) = make_uint4(a0, a1, a2, a3);
         }
       }
       sm100::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&v_full[st]);
-      if (tile + 1 < T) load_v(tile + 1);
+      if (tile + 1 < T) load_v();
 #pragma unroll
       for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
     }
