@@ -62,32 +62,6 @@ constexpr int smem_bytes() {
   return 1024 + (MT + 4) * kOpBytes + kTabs * 4 * 16 + 256;
 }
 
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_get(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return h2(__hmul2(as_h2(a), as_h2(b)));
 }
@@ -276,12 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // busy while others of them wait for their scores or store: four warps of 32
     // rows took 2850 cycles a tile, 1024 of them exponentials.
     const int g = lane >> 2, t4 = lane & 3;
-    float crow[2], m[2];  // row factors, bounds
-    uint64_t E2[2];       // sums of even and odd columns
+    float crow[2], m[2], E[2];  // row factors, bounds, sums
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       crow[n] = __shfl_sync(0xffffffffu, cr, 16 * n + 2 * g);
-      E2[n] = 0;
+      E[n] = 0.0f;
       m[n] = 0.0f;
     }
     bool ok = true;
@@ -299,16 +272,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 32 keys share the powers of two 2^x (scale of the keys), 2^y (of the
         // values): t - m = S cr 2^x + (y - m), and E takes 2^(t - m) 2^-y
         const float4 sc = tb[c];
-        uint64_t t[2][4];  // [row][8 columns: this lane's pair]
+        // (scalar operations: the packed f32x2 forms run on one of the two FMA
+        // pipes only, which the fp16 products of the dequantization need as well;
+        // with them the largest batch took 342 us instead of 308)
+        float2 t[2][4];  // [row][8 columns: this lane's pair]
         sm100::tmem_ld_wait();
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const float cf = crow[n] * sc.x, cm = sc.y - m[n];
-          const uint64_t c2 = f2(cf, cf), m2 = f2(cm, cm);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            t[n][j] = f2_fma(f2(__uint_as_float(v[4 * j + 2 * n]),
-                                __uint_as_float(v[4 * j + 2 * n + 1])), c2, m2);
+            t[n][j] = make_float2(fmaf(__uint_as_float(v[4 * j + 2 * n]), cf, cm),
+                                  fmaf(__uint_as_float(v[4 * j + 2 * n + 1]), cf, cm));
         }
         if (c + 1 < kTile / 32) tmem_ld_16x256b_x4(ts + 32 * (c + 1), v);
         if (key_left < kTile) {  // the last tile of the prefix: columns without a key
@@ -317,45 +292,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int key = 32 * c + 8 * j + t4;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              const float2 x = f2_get(t[n][j]);
-              t[n][j] = f2(key < key_left ? x.x : -INFINITY, key + 4 < key_left ? x.y : -INFINITY);
+              if (key >= key_left) t[n][j].x = -INFINITY;
+              if (key + 4 >= key_left) t[n][j].y = -INFINITY;
             }
           }
         }
         uint32_t w[8];
-        uint64_t e2[2];
+        float2 e[2];  // [row] sums of even and odd columns
         auto weigh = [&]() {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n) {
+            e[n] = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 y = f2_get(t[n][j]);
-              const float w0 = ex2(y.x), w1 = ex2(y.y);
-              e2[n] = j == 0 ? f2(w0, w1) : f2_add(e2[n], f2(w0, w1));
+              const float w0 = ex2(t[n][j].x), w1 = ex2(t[n][j].y);
+              e[n].x += w0;
+              e[n].y += w1;
               w[2 * j + n] = pack_f16x2(w0, w1);
             }
+          }
         };
         weigh();
         // No weight is above a lane's sums of 4: while those stay below 2^11 they
         // all fit fp16, and no maximum is needed. The first columns set the
         // bound, whatever their scores.
         const bool first = i == 0 && c == 0;
-        const float2 e0 = f2_get(e2[0]), e1 = f2_get(e2[1]);
-        if (__any_sync(0xffffffffu,
-                       first || fmaxf(fmaxf(e0.x, e0.y), fmaxf(e1.x, e1.y)) > kSumMax)) {
+        const float top = fmaxf(fmaxf(e[0].x, e[0].y), fmaxf(e[1].x, e[1].y));
+        if (__any_sync(0xffffffffu, first || top > kSumMax)) {
           // a bound moves (in a row's first columns, rarely later): what was
           // summed against the old one is brought down, the weights of this
           // tile's columns before these among it
           float f[2];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float2 e = f2_get(e2[n]);
-            float mx = kNone, sum = fmaxf(e.x, e.y);
+            float mx = kNone, sum = fmaxf(e[n].x, e[n].y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 x = f2_get(t[n][j]);
-              mx = fmaxf(mx, fmaxf(x.x, x.y));
-            }
+            for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(t[n][j].x, t[n][j].y));
 #pragma unroll
             for (int o = 1; o <= 2; o <<= 1) {
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -365,10 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float up = first || sum > kSumMax ? mx : 0.0f;
             f[n] = first ? 1.0f : ex2(-up);
             m[n] += up;
-            E2[n] = f2_mul(E2[n], f2(f[n], f[n]));
-            const uint64_t u2 = f2(-up, -up);
+            E[n] *= f[n];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t[n][j] = f2_add(t[n][j], u2);
+            for (int j = 0; j < 4; ++j) {
+              t[n][j].x -= up;
+              t[n][j].y -= up;
+            }
           }
           if (i > 0) {
 #pragma unroll 1
@@ -397,9 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           weigh();
         }
-        const uint64_t z2 = f2(sc.z, sc.z);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) E2[n] = f2_fma(e2[n], z2, E2[n]);
+        for (int n = 0; n < 2; ++n) E[n] = fmaf(e[n].x + e[n].y, sc.z, E[n]);
         tmem_st_16x128b_x4(ts + 16 * c, w);  // over columns whose scores were read
       }
       sm100::tmem_st_wait();
@@ -423,8 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = base + 8 * n + g;
         have[n] = row < nrows;
         at[n] = ((int64_t)(row / p.R) * p.Hq + kh * p.R + row % p.R) * nslot + slot;
-        const float2 e2 = f2_get(E2[n]);
-        float e = e2.x + e2.y;
+        float e = E[n];
         e += __shfl_xor_sync(0xffffffffu, e, 1);
         e += __shfl_xor_sync(0xffffffffu, e, 2);
         if (t4 == 0 && have[n]) p.stat[at[n]] = make_float2(i > 0 ? m[n] : kNone, e);
