@@ -49,42 +49,62 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// One step's 32 keys as they come from memory. Lane (g, t4) holds the K rows
-// of tokens 4 g .. 4 g + 3 (16 bytes of each: dimensions 32 t4 ..), the V
-// words of block t4 (dimensions 32 j + 4 g ..), and the scales of its tokens.
-struct Raw {
-  uint4 k[4], v[4];
-  uint2 sk, zk, sv, zv;  // 4 fp16 each
-};
+// A warp's steps (32 keys each) go through a ring of its own in shared memory:
+// two steps are in flight by cp.async while one is computed, and nothing but the
+// warp itself waits for them. A stage holds 32 K rows of 64 bytes and 4 V blocks
+// of 512. Lane (g, t4) reads the K rows of tokens 4 g .. 4 g + 3 (16 bytes of
+// each: dimensions 32 t4 ..) and the V words of block t4 (dimensions 32 j + 4 g
+// ..): row r is kept at place r ^ (r / 4 % 2), piece q of block t4 at q ^ 2 t4,
+// so that the 8 lanes of a phase read distinct banks. The step's scales and
+// zeros, which may lie at any 2-byte address, are loaded a step ahead in
+// registers (a token a lane) and put beside.
+constexpr int kStages = 3;
+constexpr int kStageBytes = kStep * kD;                    // codes of 32 keys, K and V
+constexpr int kScaleBytes = 4 * kStep * 2;                 // sk, zk, sv, zv
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
-__device__ __forceinline__ uint2 load4(const __half* p, int64_t at, int n, bool vec, uint32_t pad) {
-  if (vec) return *reinterpret_cast<const uint2*>(p + at);
-  const uint16_t* u = reinterpret_cast<const uint16_t*>(p) + at;
-  const uint32_t a = n > 0 ? u[0] : pad, b = n > 1 ? u[1] : pad;
-  const uint32_t c = n > 2 ? u[2] : pad, d = n > 3 ? u[3] : pad;
-  return make_uint2(a | (b << 16), c | (d << 16));
+template <int NT>
+constexpr int attn_smem() {  // ring, scales (two steps), query fragments, statistics
+  return kRingBytes + kWarps * 2 * kScaleBytes + (NT > 1 ? NT * 2048 : 0) + 2 * kWarps * 8 * NT * 4;
+}
+// the warps' output rows use the ring's space at the end
+constexpr int kOutPitch = kD + 4;
+static_assert(kWarps * 2 * 8 * kOutPitch * 4 <= kRingBytes, "two groups of 8 rows");
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
 }
 
-// Step at token l0 of the cache row block that starts at row0 (V: vrow0);
-// tokens from `end` on give zero codes, scale 1 and zero 0.
-__device__ __forceinline__ void load_step(Raw& w, const Cache& c, int64_t row0, int64_t vrow0,
-                                          int l0, int end, int g, int t4, bool vec4) {
-  const int tok = l0 + 4 * g;
+// Codes of the step at token l0 into a stage (tokens from `end` on: zeros).
+__device__ __forceinline__ void load_codes(uint32_t stage, const Cache& c, int64_t crow0,
+                                           int64_t vrow0, int l0, int end, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w.k[i] = tok + i < end ? ld_stream_u4(c.kc + (row0 + tok + i) * (kD / 8) + 4 * t4)
-                           : make_uint4(0, 0, 0, 0);
-  const int blk = (l0 >> 3) + t4;
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const bool in = l0 + r < end;
+    cp_async16(stage + (uint32_t)((r ^ ((r >> 2) & 1)) * 64 + 16 * (lane & 3)),
+               c.kc + (crow0 + (in ? l0 + r : 0)) * (kD / 8) + 4 * (lane & 3), in);
+  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w.v[j] = 8 * blk < end ? ld_stream_u4(c.vc + (vrow0 + blk) * kD + 32 * j + 4 * g)
-                           : make_uint4(0, 0, 0, 0);
-  const bool vec = vec4 && l0 + kStep <= end;
-  const int n = end - tok;
-  w.sk = load4(c.ks, row0 + tok, n, vec, 0x3C00u);
-  w.zk = load4(c.kz, row0 + tok, n, vec, 0u);
-  w.sv = load4(c.vs, row0 + tok, n, vec, 0x3C00u);
-  w.zv = load4(c.vz, row0 + tok, n, vec, 0u);
+  for (int i = 0; i < 4; ++i) {
+    const int blk = (l0 >> 3) + i;
+    const bool in = 8 * blk < end;
+    cp_async16(stage + (uint32_t)(kStep * 64 + i * 512 + ((lane ^ (2 * i)) << 4)),
+               c.vc + (vrow0 + (in ? blk : 0)) * kD + 4 * lane, in);
+  }
+}
+
+// The lane's token of the step at l0: sk, zk, sv, zv as bits (from `end` on: 1 and 0).
+__device__ __forceinline__ void load_scales(uint16_t (&s)[4], const Cache& c, int64_t crow0, int l0,
+                                            int end, int lane) {
+  const bool in = l0 + lane < end;
+  const int64_t at = crow0 + l0 + lane;
+  s[0] = in ? reinterpret_cast<const uint16_t*>(c.ks)[at] : (uint16_t)0x3C00u;
+  s[1] = in ? reinterpret_cast<const uint16_t*>(c.kz)[at] : (uint16_t)0;
+  s[2] = in ? reinterpret_cast<const uint16_t*>(c.vs)[at] : (uint16_t)0x3C00u;
+  s[3] = in ? reinterpret_cast<const uint16_t*>(c.vz)[at] : (uint16_t)0;
 }
 
 // The query rows row0 + n (n < nrows, at most 8 NT) of KV head kh against keys
@@ -92,21 +112,38 @@ __device__ __forceinline__ void load_step(Raw& w, const Cache& c, int64_t row0, 
 template <int NT>
 __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int64_t crow0,
                                        int64_t vrow0, int kh, int row0, int nrows, int begin,
-                                       int end, int slot, float* sm) {
+                                       int end, int slot, uint8_t* sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const bool vec4 = (crow0 & 3) == 0;
-
-  Raw cur;
+  const uint32_t ring = smem_u32(sm) + (uint32_t)(warp * kStages * kStageBytes);
+  const uint8_t* ring_p = sm + warp * kStages * kStageBytes;
+  uint16_t* scl = reinterpret_cast<uint16_t*>(sm + kRingBytes + warp * 2 * kScaleBytes);
+  uint2* qsm = reinterpret_cast<uint2*>(sm + kRingBytes + kWarps * 2 * kScaleBytes);
+  float* msm = reinterpret_cast<float*>(sm + kRingBytes + kWarps * 2 * kScaleBytes +
+                                        (NT > 1 ? NT * 2048 : 0));  // [warps][8 NT] m, then E
+  constexpr int kStride = kWarps * kStep;
   int l0 = begin + warp * kStep;
-  if (l0 < end) load_step(cur, c, crow0, vrow0, l0, end, g, t4, vec4);
+  uint16_t sc4[4];
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (l0 + s * kStride < end)
+      load_codes(ring + s * kStageBytes, c, crow0, vrow0, l0 + s * kStride, end, lane);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  if (l0 < end) {
+    load_scales(sc4, c, crow0, l0, end, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) scl[i * kStep + lane] = sc4[i];
+    if (l0 + kStride < end) load_scales(sc4, c, crow0, l0 + kStride, end, lane);
+  }
 
   // Query fragments (B operand, column n = row): dimensions 32 t4 + 8 j + ..
   // in the order of the code words' nibbles. The row's power of two goes to
   // the score factor of rows 2 t4 and 2 t4 + 1, the accumulator's columns.
-  uint32_t bq[NT][8][2];
+  // Eight rows stay in registers; more are read again at every step.
+  constexpr bool kQSmem = NT > 1;
+  uint32_t bq[kQSmem ? 1 : 8][2];
   float cr[NT][2];
-#pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int n = 8 * nt + g;
     float f[32];
@@ -145,14 +182,27 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        uint32_t b[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          bq[nt][2 * j + e][b] = pack_f16x2(f[8 * j + 2 * e + b] * up, f[8 * j + 2 * e + b + 4] * up);
+        for (int h = 0; h < 2; ++h)
+          b[h] = pack_f16x2(f[8 * j + 2 * e + h] * up, f[8 * j + 2 * e + h + 4] * up);
+        if (kQSmem) {
+          // every warp has the same fragments: one of them writes
+          if (warp == nt % kWarps) qsm[(nt * 8 + 2 * j + e) * 32 + lane] = make_uint2(b[0], b[1]);
+        } else {
+          bq[kQSmem ? 0 : 2 * j + e][0] = b[0];
+          bq[kQSmem ? 0 : 2 * j + e][1] = b[1];
+        }
+      }
     const float fac = down * kScoreScale;
-    cr[nt][0] = __shfl_sync(0xffffffffu, fac, (2 * t4) * 4);
-    cr[nt][1] = __shfl_sync(0xffffffffu, fac, (2 * t4 + 1) * 4);
+    const float c0 = __shfl_sync(0xffffffffu, fac, (2 * t4) * 4);
+    const float c1 = __shfl_sync(0xffffffffu, fac, (2 * t4 + 1) * 4);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (i == nt) cr[i][0] = c0, cr[i][1] = c1;
   }
+  if (kQSmem) __syncthreads();
 
   float O[NT][8][4];
   float m[NT][2], E[NT][2];
@@ -166,44 +216,39 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
     E[nt][0] = E[nt][1] = 0.0f;
   }
 
-  for (; l0 < end; l0 += kWarps * kStep) {
+  for (int k = 0; l0 < end; l0 += kStride, ++k) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // the step is complete, and the stage of the step before is read
+    if (l0 + (kStages - 1) * kStride < end)
+      load_codes(ring + (uint32_t)((k + kStages - 1) % kStages) * kStageBytes, c, crow0, vrow0,
+                 l0 + (kStages - 1) * kStride, end, lane);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (l0 + kStride < end) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) scl[((k + 1) & 1) * (4 * kStep) + i * kStep + lane] = sc4[i];
+      if (l0 + 2 * kStride < end) load_scales(sc4, c, crow0, l0 + 2 * kStride, end, lane);
+    }
+    const uint8_t* stage = ring_p + (k % kStages) * kStageBytes;
+    const uint16_t* sp = scl + (k & 1) * (4 * kStep);
+    const uint2 ssk = *reinterpret_cast<const uint2*>(sp + 4 * g);
+    const uint2 szk = *reinterpret_cast<const uint2*>(sp + kStep + 4 * g);
+    const uint2 ssv = *reinterpret_cast<const uint2*>(sp + 2 * kStep + 4 * g);
+    const uint4 szv = *reinterpret_cast<const uint4*>(sp + 3 * kStep + 8 * t4);
     // ---- scores: S^T tile s holds tokens 4 g + 2 s (rows g) and + 1 (rows
     // g + 8) against the query rows 2 t4, 2 t4 + 1
     float sc[NT][2][4];
-    const uint32_t zk2[4] = {prmt(cur.zk.x, 0, 0x1010), prmt(cur.zk.x, 0, 0x3232),
-                             prmt(cur.zk.y, 0, 0x1010), prmt(cur.zk.y, 0, 0x3232)};
+    const uint32_t zk2[4] = {prmt(szk.x, 0, 0x1010), prmt(szk.x, 0, 0x3232),
+                             prmt(szk.y, 0, 0x1010), prmt(szk.y, 0, 0x3232)};
     uint32_t z1[4], z64[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       z1[i] = h2(__hadd2(as_h2(zk2[i]), as_h2(0x64006400u)));
       z64[i] = h2(__hneg2(__hadd2(as_h2(zk2[i]), as_h2(0x54005400u))));
     }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sc[nt][s][r] = 0.0f;
-      const uint32_t ka[4] = {cur.k[2 * s].x, cur.k[2 * s].y, cur.k[2 * s].z, cur.k[2 * s].w};
-      const uint32_t kb[4] = {cur.k[2 * s + 1].x, cur.k[2 * s + 1].y, cur.k[2 * s + 1].z,
-                              cur.k[2 * s + 1].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t a0, a1, a2, a3;
-          codes_f16(e ? ka[j] >> 8 : ka[j], z1[2 * s], z64[2 * s], a0, a2);
-          codes_f16(e ? kb[j] >> 8 : kb[j], z1[2 * s + 1], z64[2 * s + 1], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(sc[nt][s], a0, a1, a2, a3, bq[nt][2 * j + e][0], bq[nt][2 * j + e][1]);
-        }
-    }
-    // ---- weights
     float skf[4], lsv[4], rsv[4];
     {
-      const float2 s01 = __half22float2(as_h2(cur.sk.x)), s23 = __half22float2(as_h2(cur.sk.y));
-      const float2 v01 = __half22float2(as_h2(cur.sv.x)), v23 = __half22float2(as_h2(cur.sv.y));
+      const float2 s01 = __half22float2(as_h2(ssk.x)), s23 = __half22float2(as_h2(ssk.y));
+      const float2 v01 = __half22float2(as_h2(ssv.x)), v23 = __half22float2(as_h2(ssv.y));
       skf[0] = s01.x, skf[1] = s01.y, skf[2] = s23.x, skf[3] = s23.y;
       const float v[4] = {v01.x, v01.y, v23.x, v23.y};
 #pragma unroll
@@ -213,6 +258,43 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
         rsv[i] = ex2(-lsv[i]);
       }
     }
+    uint32_t y1[2], y64[2];  // k-step s: zeros of tokens (2s, 2s + 4), and (2s + 1, 2s + 5)
+    y1[0] = h2(__hadd2(as_h2(prmt(szv.x, szv.z, 0x5410)), as_h2(0x64006400u)));
+    y1[1] = h2(__hadd2(as_h2(prmt(szv.y, szv.w, 0x5410)), as_h2(0x64006400u)));
+    y64[0] = h2(__hneg2(__hadd2(as_h2(prmt(szv.x, szv.z, 0x7632)), as_h2(0x54005400u))));
+    y64[1] = h2(__hneg2(__hadd2(as_h2(prmt(szv.y, szv.w, 0x7632)), as_h2(0x54005400u))));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sc[nt][s][r] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint4 ra = *reinterpret_cast<const uint4*>(
+          stage + ((4 * g + 2 * s) ^ (g & 1)) * 64 + 16 * t4);
+      const uint4 rb = *reinterpret_cast<const uint4*>(
+          stage + ((4 * g + 2 * s + 1) ^ (g & 1)) * 64 + 16 * t4);
+      const uint32_t ka[4] = {ra.x, ra.y, ra.z, ra.w}, kb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t a0, a1, a2, a3;
+          codes_f16(e ? ka[j] >> 8 : ka[j], z1[2 * s], z64[2 * s], a0, a2);
+          codes_f16(e ? kb[j] >> 8 : kb[j], z1[2 * s + 1], z64[2 * s + 1], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint2 q;
+            if (kQSmem)
+              q = qsm[(nt * 8 + 2 * j + e) * 32 + lane];
+            else
+              q = make_uint2(bq[kQSmem ? 0 : 2 * j + e][0], bq[kQSmem ? 0 : 2 * j + e][1]);
+            mma16816(sc[nt][s], a0, a1, a2, a3, q.x, q.y);
+          }
+        }
+    }
+    // ---- weights
     const int left = end - (l0 + 4 * g);  // this lane's tokens i < left exist
     bool grow = false;
 #pragma unroll
@@ -261,21 +343,12 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
         bp[nt][s][0] = transpose8x8(pack_f16x2(w[0], w[1]));
         bp[nt][s][1] = transpose8x8(pack_f16x2(w[2], w[3]));
       }
-    // ---- values: zeros of block t4's tokens come from lanes g = 2 t4, 2 t4 + 1
-    uint32_t y1[2], y64[2];  // k-step s: tokens (2s, 2s + 4), and (2s + 1, 2s + 5)
-    {
-      const uint32_t ax = __shfl_sync(0xffffffffu, cur.zv.x, 8 * t4);
-      const uint32_t ay = __shfl_sync(0xffffffffu, cur.zv.y, 8 * t4);
-      const uint32_t bx = __shfl_sync(0xffffffffu, cur.zv.x, 8 * t4 + 4);
-      const uint32_t by = __shfl_sync(0xffffffffu, cur.zv.y, 8 * t4 + 4);
-      y1[0] = h2(__hadd2(as_h2(prmt(ax, bx, 0x5410)), as_h2(0x64006400u)));
-      y1[1] = h2(__hadd2(as_h2(prmt(ay, by, 0x5410)), as_h2(0x64006400u)));
-      y64[0] = h2(__hneg2(__hadd2(as_h2(prmt(ax, bx, 0x7632)), as_h2(0x54005400u))));
-      y64[1] = h2(__hneg2(__hadd2(as_h2(prmt(ay, by, 0x7632)), as_h2(0x54005400u))));
-    }
+    // ---- values
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t vw[4] = {cur.v[j].x, cur.v[j].y, cur.v[j].z, cur.v[j].w};
+      const uint4 rv = *reinterpret_cast<const uint4*>(
+          stage + kStep * 64 + t4 * 512 + (((8 * j + g) ^ (2 * t4)) << 4));
+      const uint32_t vw[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -288,14 +361,13 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
             mma16816(O[nt][2 * j + e], a0, a1, a2, a3, bp[nt][s][0], bp[nt][s][1]);
         }
     }
-    if (l0 + kWarps * kStep < end)
-      load_step(cur, c, crow0, vrow0, l0 + kWarps * kStep, end, g, t4, vec4);
   }
 
   // ---- the warps' results: E over the lanes of a column, then O and E over
   // the warps against their common bound
-  float* osm = sm;                                  // [8 NT rows][128 + 4]
-  float* msm = sm + 8 * NT * (kD + 4);              // [warps][8 NT] m, then E
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();                                  // the rings are read: their space is free
+  float* osm = reinterpret_cast<float*>(sm);        // [warps][8 NT rows][kOutPitch]
   float* esm = msm + kWarps * 8 * NT;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -320,29 +392,30 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
       for (int w = 0; w < kWarps; ++w) big = fmaxf(big, msm[w * 8 * NT + 8 * nt + 2 * t4 + x]);
       f[nt][x] = ex2(m[nt][x] - big);
     }
-  // the warps add up in order, so that the sum does not depend on their timing
-  for (int w = 0; w < kWarps; ++w) {
-    if (warp == w) {
+  // each warp puts its rows down, then the warps' parts are added in order
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int d = 32 * (i >> 1) + 4 * g + 2 * (i & 1) + (r >> 1);
-            float* at = osm + (8 * nt + 2 * t4 + (r & 1)) * (kD + 4) + d;
-            const float v = O[nt][i][r] * f[nt][r & 1];
-            *at = w == 0 ? v : *at + v;
-          }
-    }
-    __syncthreads();
-  }
+      for (int r = 0; r < 4; ++r) {
+        const int d = 32 * (i >> 1) + 4 * g + 2 * (i & 1) + (r >> 1);
+        osm[(warp * 8 * NT + 8 * nt + 2 * t4 + (r & 1)) * kOutPitch + d] =
+            O[nt][i][r] * f[nt][r & 1];
+      }
+  __syncthreads();
   const int nslot = p.nsp + p.nso;
   for (int n = warp; n < nrows; n += kWarps) {
     const int row = row0 + n;
     const int64_t at = ((int64_t)(row / p.R) * p.Hq + kh * p.R + row % p.R) * nslot + slot;
-    *reinterpret_cast<float4*>(p.part + at * kD + 4 * lane) =
-        *reinterpret_cast<const float4*>(osm + n * (kD + 4) + 4 * lane);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float4 x =
+          *reinterpret_cast<const float4*>(osm + (w * 8 * NT + n) * kOutPitch + 4 * lane);
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    *reinterpret_cast<float4*>(p.part + at * kD + 4 * lane) = v;
     if (lane == 0) {
       float big = kNone, e = 0.0f;
 #pragma unroll
@@ -363,19 +436,21 @@ __device__ __forceinline__ int own_length(const PrefixArgs& p, int b) {
 // where the tcgen05 kernel takes it: nprefix is 0 here); the rest: key range x
 // KV head x sequence of the own tokens. Launched while the tcgen05 kernel still
 // runs, whose results the merge needs too: every CTA ends by waiting for it.
-template <int NT>
-__global__ void __launch_bounds__(32 * kWarps)
+template <int NTP, int NTO>
+__global__ void __launch_bounds__(32 * kWarps, NTP * NTO == 1 ? 4 : 2)
     prefix_attn_kernel(const __grid_constant__ PrefixArgs p, int nprefix) {
-  __shared__ __align__(16) float sm[8 * NT * (kD + 4) + 2 * kWarps * 8 * NT];
+  extern __shared__ __align__(16) uint8_t sm[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int i = blockIdx.x;
   if (i < nprefix) {
-    const int slot = i % p.nsp;
-    const int rt = (i / p.nsp) % p.nrt;
-    const int kh = i / (p.nsp * p.nrt);
+    const int ranges = p.nsp;
+    const int slot = i % ranges;
+    const int rt = (i / ranges) % p.nrt;
+    const int kh = i / (ranges * p.nrt);
     const int begin = slot * p.chunk_p;
-    attend<NT>(p, p.pre, kh * p.pre.cap, kh * p.pre.nblk, kh, rt * 8 * NT,
-               min(8 * NT, p.B * p.R - rt * 8 * NT), begin, min(begin + p.chunk_p, p.P), slot, sm);
+    attend<NTP>(p, p.pre, kh * p.pre.cap, kh * p.pre.nblk, kh, rt * 8 * NTP,
+                min(8 * NTP, p.B * p.R - rt * 8 * NTP), begin, min(begin + p.chunk_p, p.P), slot,
+                sm);
   } else {
     i -= nprefix;
     const int range = i % p.nso;
@@ -385,37 +460,89 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int begin = range * p.chunk_o;
     const int64_t bh = (int64_t)b * p.Hkv + kh;
     if (begin < len)
-      attend<NT>(p, p.own, bh * p.own.cap, bh * p.own.nblk, kh, b * p.R, p.R, begin,
-                 min(begin + p.chunk_o, len), p.nsp + range, sm);
+      attend<NTO>(p, p.own, bh * p.own.cap, bh * p.own.nblk, kh, b * p.R, p.R, begin,
+                  min(begin + p.chunk_o, len), p.nsp + range, sm);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// One warp a row: the ranges' partial results against their common bound.
-__global__ void __launch_bounds__(128) prefix_merge_kernel(const __grid_constant__ PrefixArgs p) {
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= p.B * p.Hq) return;
-  const int b = row / p.Hq;
-  const int n = p.nsp + (own_length(p, b) + p.chunk_o - 1) / p.chunk_o;
+// The ranges' partial results of a row against their common bound. W warps a
+// row, each a run of the ranges: 4 where there are many ranges (a single warp
+// that walked 30 to 60 of them one by one took 12 us), one where there are few
+// and the rows fill the GPU. A lane takes one range's statistics, and four
+// partial rows are in flight at once.
+constexpr int kMergeWarps = 4;
+template <int W>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    prefix_merge_kernel(const __grid_constant__ PrefixArgs p) {
+  __shared__ float4 acc[kMergeWarps][32];
+  __shared__ float2 top[kMergeWarps];  // (bound, E) of each warp's ranges
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * (kMergeWarps / W) + warp / W, part = warp % W;
+  const bool have = row < p.B * p.Hq;
+  const int n = have ? p.nsp + (own_length(p, row / p.Hq) + p.chunk_o - 1) / p.chunk_o : 0;
   const int64_t base = (int64_t)row * (p.nsp + p.nso);
+  const int run = (n + W - 1) / W;
+  const int end = min((part + 1) * run, n);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  float big = kNone;
-  for (int j = lane; j < n; j += 32) big = fmaxf(big, p.stat[base + j].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+  float m = kNone, e = 0.0f;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float e = 0.0f;
-  for (int j = 0; j < n; ++j) {
-    const float2 st = p.stat[base + j];
-    if (st.y == 0.0f) continue;  // a range without keys wrote no partial result
-    const float f = ex2(st.x - big);
-    const float4 v = *reinterpret_cast<const float4*>(p.part + (base + j) * kD + 4 * lane);
-    a.x = fmaf(f, v.x, a.x);
-    a.y = fmaf(f, v.y, a.y);
-    a.z = fmaf(f, v.z, a.z);
-    a.w = fmaf(f, v.w, a.w);
-    e = fmaf(f, st.y, e);
+  for (int j0 = part * run; j0 < end; j0 += 32) {
+    const int cnt = min(32, end - j0);
+    // a range without keys wrote (kNone, 0) and no partial row
+    const float2 st = lane < cnt ? p.stat[base + j0 + lane] : make_float2(kNone, 0.0f);
+    const float* src = p.part + (base + j0) * kD + 4 * lane;
+    float big = fmaxf(m, st.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const float f = st.y == 0.0f ? 0.0f : ex2(st.x - big);
+    const float old = ex2(m - big);
+    m = big;
+    e = fmaf(e, old, f * st.y);  // per lane, summed at the end
+    a.x *= old, a.y *= old, a.z *= old, a.w *= old;
+    for (int j = 0; j < cnt; j += 4) {
+      float4 v[4];
+      float g[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, (j + i) & 31);
+        g[i] = j + i < cnt ? w : 0.0f;
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (g[i] != 0.0f) v[i] = *reinterpret_cast<const float4*>(src + (int64_t)(j + i) * kD);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a.x = fmaf(g[i], v[i].x, a.x);
+        a.y = fmaf(g[i], v[i].y, a.y);
+        a.z = fmaf(g[i], v[i].z, a.z);
+        a.w = fmaf(g[i], v[i].w, a.w);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+  if (W > 1) {
+    acc[warp][lane] = a;
+    if (lane == 0) top[warp] = make_float2(m, e);
+    __syncthreads();
+    if (part != 0) return;
+    float big = kNone;
+#pragma unroll
+    for (int w = 0; w < W; ++w) big = fmaxf(big, top[warp + w].x);
+    a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    e = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = ex2(top[warp + w].x - big);
+      const float4 v = acc[warp + w][lane];
+      e = fmaf(f, top[warp + w].y, e);
+      a.x = fmaf(f, v.x, a.x);
+      a.y = fmaf(f, v.y, a.y);
+      a.z = fmaf(f, v.z, a.z);
+      a.w = fmaf(f, v.w, a.w);
+    }
+  }
+  if (!have) return;
   const float inv = n > 0 ? 1.0f / e : 0.0f;  // a row with no key at all: zeros
   const float x[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
   uint2 o;
@@ -426,10 +553,17 @@ __global__ void __launch_bounds__(128) prefix_merge_kernel(const __grid_constant
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)row * kD + 4 * lane) = o;
 }
 
+// Rows of a KV head from which on the prefix goes to the tensor cores of
+// tcgen05. 32768 keys x 8 heads: 16 rows 31 us on mma.sync and 40 on tcgen05,
+// 24 rows 45 (three or four groups of 8) and 40.
+constexpr int64_t kTcRows = 17;
+
 // How a problem is cut: the same for the workspace query and the launch.
 struct Plan {
-  int tc;  // row tiles of a tcgen05 CTA (1 or 2), or 0: the prefix on mma.sync
-  int nt, nrt, chunk_p, ranges, nsp, chunk_o, nso;
+  int tc;   // row tiles of a tcgen05 CTA (1 or 2), or 0: the prefix on mma.sync
+  int ntp;  // 8-row groups of a prefix row tile on mma.sync
+  int nto;  // of a sequence's own rows
+  int nrt, chunk_p, ranges, nsp, chunk_o, nso;
 };
 
 Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
@@ -443,12 +577,13 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
     chunk = (int)(((keys + ranges - 1) / ranges + step - 1) / step * step);
     n = (int)((keys + chunk - 1) / chunk);
   };
-  pl.nt = R <= 8 ? 1 : 2;
+  pl.nto = R <= 8 ? 1 : 2;
+  pl.ntp = rows <= 8 ? 1 : 2;
   pl.tc = 0;
   pl.nsp = pl.ranges = 0;
   pl.nrt = 0;
   pl.chunk_p = 128;
-  if (P > 0 && rows > 16) {
+  if (P > 0 && rows >= kTcRows) {
     // tcgen05: the ranges that give the slowest SM the least work, a CTA's
     // start and end counted as 4 tiles
     const int64_t tiles = (P + 127) / 128, rt = (rows + 127) / 128;
@@ -466,7 +601,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
     pl.ranges = (int)((P + pl.chunk_p - 1) / pl.chunk_p);
     pl.nsp = pl.tc == 1 ? 2 * pl.ranges : pl.ranges;
   } else if (P > 0) {
-    pl.nrt = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+    pl.nrt = (int)((rows + 8 * pl.ntp - 1) / (8 * pl.ntp));
     cut(P, std::max<int64_t>(1, Hkv * pl.nrt), pl.chunk_p, pl.ranges);
     pl.nsp = pl.ranges;
   }
@@ -474,7 +609,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
   return pl;
 }
 
-template <int NT>
+template <int NTP, int NTO>
 wq_status launch(const PrefixArgs& a, int tc, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -488,15 +623,34 @@ wq_status launch(const PrefixArgs& a, int tc, cudaStream_t st) {
     cfg.numAttrs = 1;
   }
   const int nprefix = tc ? 0 : a.nprefix;
+  constexpr int kSmem = attn_smem<(NTP > NTO ? NTP : NTO)>();
+  static bool attr_set = [] {
+    return cudaFuncSetAttribute(prefix_attn_kernel<NTP, NTO>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess;
+  }();
+  if (!attr_set) return WQ_ERR_CUDA;
   cfg.gridDim = dim3((unsigned)(nprefix + (int64_t)a.nso * a.Hkv * a.B), 1, 1);
   cfg.blockDim = dim3(32 * kWarps, 1, 1);
-  if (cudaLaunchKernelEx(&cfg, prefix_attn_kernel<NT>, a, nprefix) != cudaSuccess)
+  cfg.dynamicSmemBytes = kSmem;
+  if (cudaLaunchKernelEx(&cfg, prefix_attn_kernel<NTP, NTO>, a, nprefix) != cudaSuccess)
     return WQ_ERR_CUDA;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq + 3) / 4), 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  if (cudaLaunchKernelEx(&cfg, prefix_merge_kernel, a) != cudaSuccess) return WQ_ERR_CUDA;
+  const int64_t rows = (int64_t)a.B * a.Hq;
+  const int warps = a.nsp + a.nso <= 12 ? 1 : kMergeWarps;
+  cfg.gridDim = dim3((unsigned)((rows * warps + kMergeWarps - 1) / kMergeWarps), 1, 1);
+  cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&cfg, warps == 1 ? prefix_merge_kernel<1> : prefix_merge_kernel<kMergeWarps>,
+                         a) != cudaSuccess)
+    return WQ_ERR_CUDA;
   return launch_status();
+}
+
+template <int NTO>
+wq_status launch_o(const PrefixArgs& a, const Plan& pl, cudaStream_t st) {
+  // (R > 8 has more than 8 rows: a prefix on mma.sync then takes two groups)
+  if (NTO == 1 && (pl.tc || pl.ntp == 1)) return launch<1, 1>(a, pl.tc, st);
+  return launch<2, NTO>(a, pl.tc, st);
 }
 
 }  // namespace
@@ -538,7 +692,7 @@ wq_status launch_prefix_attn(const void* q, wq_dtype dt, int64_t q_stride, int64
   a.part = static_cast<float*>(workspace);
   a.stat = reinterpret_cast<float2*>(a.part + (size_t)B * Hq * (pl.nsp + pl.nso) * kD);
   a.out = out;
-  return pl.nt == 1 ? launch<1>(a, pl.tc, st) : launch<2>(a, pl.tc, st);
+  return pl.nto == 1 ? launch_o<1>(a, pl, st) : launch_o<2>(a, pl, st);
 }
 
 }  // namespace wq

@@ -319,7 +319,7 @@ def test_refusals(wq):
                                v, ln)
 
 
-@pytest.mark.parametrize("b", [8, 40])
+@pytest.mark.parametrize("b", [8, 40])  # 64 and 320 query rows: one and two row tiles
 def test_bounded_wait_expires_cleanly(wq, b):
     """With the first key tile withheld the tensor-core kernel gives up, reports
     the wait and returns; the next call is right."""
