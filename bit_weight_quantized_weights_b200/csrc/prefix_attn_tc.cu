@@ -201,9 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4* src = reinterpret_cast<const uint4*>(
           static_cast<const uint16_t*>(p.q) +
           (have ? (int64_t)(row / p.R) * p.q_stride + (int64_t)(kh * p.R + row % p.R) * kD : 0));
-      auto values = [&](int j, float (&f)[8]) {
-        const uint4 v = have ? src[j] : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      // (one round of loads: this latency starts the whole pipeline)
+      uint4 v[kD / 16];
+#pragma unroll
+      for (int j = 0; j < kD / 16; ++j)
+        v[j] = have ? src[8 * part + j] : make_uint4(0, 0, 0, 0);
+      auto values = [&](const uint4& x, float (&f)[8]) {
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (p.fp16) {
@@ -217,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       float amax = 0.0f, up, down;
-#pragma unroll 2
+#pragma unroll
       for (int j = 0; j < kD / 16; ++j) {
         float f[8];
-        values(8 * part + j, f);
+        values(v[j], f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
       }
@@ -229,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       cr = down * kScoreScale;
       if (MT == 2 || s == 0) {
         uint8_t* dst = sq + s * kOpBytes + part * kAtomBytes + r * 128;
-#pragma unroll 2
+#pragma unroll
         for (int j = 0; j < kD / 16; ++j) {
           float f[8];
-          values(8 * part + j, f);
+          values(v[j], f);
           *reinterpret_cast<uint4*>(dst + ((j ^ (r & 7)) << 4)) =
               make_uint4(pack_f16x2(f[0] * up, f[4] * up), pack_f16x2(f[1] * up, f[5] * up),
                          pack_f16x2(f[2] * up, f[6] * up), pack_f16x2(f[3] * up, f[7] * up));
@@ -257,11 +261,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       E[n] = 0.0f;
       m[n] = 0.0f;
     }
+    // a warp whose 16 rows are all past the batch leaves its weights as they are
+    const bool idle = base >= nrows;
     bool ok = true;
     int i = 0;
     for (int tile = MT == 2 ? 0 : s; tile < T; tile += MT == 2 ? 1 : 2, ++i) {
       ok = wait(&s_full[s], (uint32_t)i, 0x4101u);
       if (!ok) break;
+      if (idle) {
+        if (lane == 0) {
+          sm100::mbar_arrive(&p_full[s]);
+          sm100::mbar_arrive(&t_empty[tile % kTabs]);
+        }
+        continue;
+      }
       sm100::tc_fence_after();
       const int key_left = end - begin - tile * kTile;
       const float4* tb = tab + (tile % kTabs) * 4;
