@@ -143,6 +143,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The current device and a device's current stream, as integers: a call of a few
+# microseconds on the GPU is launched from here, and the Stream objects of
+# torch.cuda.current_stream() cost as much as the launch.
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_on(dev, stream):
+    return stream.cuda_stream if stream is not None else _raw_stream(dev)
+
+
 def _cuda(t, dtype, name):
     if t is None:
         return
@@ -442,24 +453,27 @@ def wq_mx_gemv(x, n, n_passes, codes, scales, workspace=None, out=None, stream=N
 def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     """MXFP4 activations kept in 4 bits: x [M, K] (bf16, fp16 or fp32; rows may
     be strided) -> (planes uint8 [P, M, K/2], scale bytes uint8 [P, M, K/32])."""
-    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() != 2:
-        raise ValueError("x must be a 2-D bfloat16, float16 or float32 CUDA tensor")
-    m, k = x.shape
-    if x.stride(1) != 1 and k > 1:
+    dev = _current_device()
+    dt, shape, xs = _DTYPES.get(x.dtype), x.shape, x.stride()
+    if dt is None or len(shape) != 2:
+        raise ValueError("x must be a 2-D bfloat16, float16 or float32 tensor")
+    m, k = shape
+    if xs[1] != 1 and k > 1:
         raise ValueError("the rows of x must be contiguous")
     if planes is None:
-        planes = torch.empty(n_planes, m, k // 2, dtype=torch.uint8, device=x.device)
+        planes = torch.empty((n_planes, m, k // 2), dtype=torch.uint8, device=x.device)
+    elif planes.dtype is not torch.uint8 or planes.shape != (n_planes, m, k // 2) or \
+            not planes.is_contiguous():
+        raise ValueError("planes must be uint8 [%d, %d, %d]" % (n_planes, m, k // 2))
     if scales is None:
-        scales = torch.empty(n_planes, m, k // 32, dtype=torch.uint8, device=x.device)
-    _cuda(planes, torch.uint8, "planes")
-    _cuda(scales, torch.uint8, "scales")
-    if planes.shape != (n_planes, m, k // 2) or scales.shape != (n_planes, m, k // 32):
-        raise ValueError("planes must be [%d, %d, %d] and scales [%d, %d, %d]"
-                         % (n_planes, m, k // 2, n_planes, m, k // 32))
-    _on_current_device(x, planes, scales)
-    _check(lib.wq_mx_quantize_planes(_ptr(x), _DTYPES[x.dtype], max(x.stride(0), k) if m < 2
-                                     else x.stride(0), m, k, n_planes, _ptr(planes), _ptr(scales),
-                                     _stream(stream)), "wq_mx_quantize_planes")
+        scales = torch.empty((n_planes, m, k // 32), dtype=torch.uint8, device=x.device)
+    elif scales.dtype is not torch.uint8 or scales.shape != (n_planes, m, k // 32) or \
+            not scales.is_contiguous():
+        raise ValueError("scales must be uint8 [%d, %d, %d]" % (n_planes, m, k // 32))
+    _on_device(dev, x, planes, scales)
+    _check(lib.wq_mx_quantize_planes(x.data_ptr(), dt, xs[0] if m > 1 else k, m, k, n_planes,
+                                     planes.data_ptr(), scales.data_ptr(),
+                                     _stream_on(dev, stream)), "wq_mx_quantize_planes")
     return planes, scales
 
 
@@ -472,28 +486,29 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
     """y bf16 [M, N] = (sum of the MXFP4 planes) . w_hat^T for any M, on the FP4
     tensor cores: planes and plane_scales as wq_mx_quantize_planes returns
     them, codes and scales as wq_mx_quantize packs the weights [N, K]."""
+    dev = _current_device()
     for t, name in ((planes, "planes"), (plane_scales, "plane_scales"), (codes, "codes"),
                     (scales, "scales")):
-        _cuda(t, torch.uint8, name)
-    if planes.dim() != 3:
+        if t.dtype is not torch.uint8 or not t.is_contiguous():
+            raise ValueError("%s must be uint8 and contiguous" % name)
+    shape = planes.shape
+    if len(shape) != 3:
         raise ValueError("planes must be [P, M, K/2]")
-    p, m, kh = planes.shape
+    p, m, kh = shape
     k = 2 * kh
     if plane_scales.shape != (p, m, k // 32) or codes.shape != (n, kh) or \
             scales.shape != (n, k // 32):
-        raise ValueError("scales or weights do not match planes %s and N = %d"
-                         % (tuple(planes.shape), n))
+        raise ValueError("scales or weights do not match planes %s and N = %d" % (tuple(shape), n))
     if workspace is None:
         workspace = mx_gemm_workspace(m, n, k, p, planes.device)
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=planes.device)
-    _cuda(out, torch.bfloat16, "y")
-    if out.shape != (m, n):
-        raise ValueError("y must be [%d, %d]" % (m, n))
-    _on_current_device(planes, plane_scales, codes, scales, workspace, out)
-    _check(lib.wq_mx_gemm(_ptr(planes), _ptr(plane_scales), m, n, k, p, _ptr(codes), _ptr(scales),
-                          _ptr(out), _ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _stream(stream)),
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=planes.device)
+    elif out.dtype is not torch.bfloat16 or out.shape != (m, n) or not out.is_contiguous():
+        raise ValueError("y must be bfloat16 [%d, %d], contiguous" % (m, n))
+    _on_device(dev, planes, plane_scales, codes, scales, workspace, out)
+    _check(lib.wq_mx_gemm(planes.data_ptr(), plane_scales.data_ptr(), m, n, k, p, codes.data_ptr(),
+                          scales.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), _stream_on(dev, stream)),
            "wq_mx_gemm")
     return out
 
@@ -546,30 +561,38 @@ def kv_quantize_values(v, stream=None):
             zr.view(b, hkv, length))
 
 
-def _on_current_device(*tensors):
+def _on_device(dev, *tensors):
     """The library launches on the current device: tensors of another are refused."""
-    dev = torch.cuda.current_device()
     for t in tensors:
-        if t.device.index != dev:
+        if t.get_device() != dev:
             raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, dev))
 
 
-def _kv_cache(k_cache, v_cache):
+def _kv_cache(k_cache, v_cache, dev):
     """Check the two parts of an INT4 cache against each other: (B, Hkv, capacity, D)."""
     kq, ks, kz = k_cache
     vq, vs, vz = v_cache
+    shape = ks.shape
+    if len(shape) == 3 and kq.dtype is torch.int32 and vq.dtype is torch.int32 and \
+            ks.dtype is torch.float16 and kz.dtype is torch.float16 and \
+            vs.dtype is torch.float16 and vz.dtype is torch.float16 and kq.is_contiguous() and \
+            vq.is_contiguous() and ks.is_contiguous() and kz.is_contiguous() and \
+            vs.is_contiguous() and vz.is_contiguous() and kz.shape == shape and \
+            vs.shape == shape and vz.shape == shape and kq.get_device() == dev and \
+            vq.get_device() == dev and ks.get_device() == dev and kz.get_device() == dev and \
+            vs.get_device() == dev and vz.get_device() == dev:
+        b, hkv, cap = shape
+        d = vq.shape[-1]
+        if kq.shape == (b, hkv, cap, d // 8) and vq.shape == (b, hkv, (cap + 7) // 8, d):
+            return b, hkv, cap, d
+    # something is wrong: say what
     for t, dt, name in ((kq, torch.int32, "k_codes"), (ks, torch.float16, "k_scales"),
                         (kz, torch.float16, "k_zeros"), (vq, torch.int32, "v_codes"),
                         (vs, torch.float16, "v_scales"), (vz, torch.float16, "v_zeros")):
         _cuda(t, dt, name)
-    if kq.dim() != 4 or ks.dim() != 3 or vq.dim() != 4:
-        raise ValueError("KV cache tensors have 4 (codes) and 3 (scales, zeros) dimensions")
-    b, hkv, cap = ks.shape
-    d = 8 * kq.shape[3]
-    if kq.shape[:3] != ks.shape or kz.shape != ks.shape or vs.shape != ks.shape or \
-            vz.shape != ks.shape or tuple(vq.shape) != (b, hkv, (cap + 7) // 8, d):
-        raise ValueError("KV cache shapes do not match each other")
-    return b, hkv, cap, d
+    _on_device(dev, *k_cache, *v_cache)
+    raise ValueError("KV cache shapes do not match: codes %s and %s, scales and zeros %s %s %s %s"
+                     % tuple(tuple(t.shape) for t in (kq, vq, ks, kz, vs, vz)))
 
 
 def kv_cache_alloc(b, hkv, capacity, d=128, device="cuda"):
@@ -583,25 +606,27 @@ def kv_cache_alloc(b, hkv, capacity, d=128, device="cuda"):
     return part(capacity, d // 8), part((capacity + 7) // 8, d)
 
 
-def _kv_rows(k, v, cache, starts, offsets):
+_Strides = ctypes.c_int64 * 2
+
+
+def _kv_rows(k, v, cache, starts, offsets, dev):
     """Check packed rows [T, Hkv, D] against a cache: (T, dtype, strides of k and v)."""
     b, hkv, _, d = cache
-    if not (k.is_cuda and v.is_cuda):
-        raise ValueError("k and v must be CUDA tensors")
-    if k.dtype not in _DTYPES or v.dtype != k.dtype:
+    shape, dt = k.shape, _DTYPES.get(k.dtype)
+    if dt is None or v.dtype is not k.dtype:
         raise ValueError("k and v must both be bfloat16, float16 or float32")
-    if k.dim() != 3 or k.shape != v.shape or k.shape[1] != hkv or k.shape[2] != d:
+    if v.shape != shape or len(shape) != 3 or shape[1] != hkv or shape[2] != d:
         raise ValueError("k and v must be [T, %d, %d], got %s and %s"
-                         % (hkv, d, tuple(k.shape), tuple(v.shape)))
-    if k.stride(2) != 1 or v.stride(2) != 1:
+                         % (hkv, d, tuple(shape), tuple(v.shape)))
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
         raise ValueError("the last dimension of k and v must be contiguous")
-    _cuda(starts, torch.int32, "starts")
-    _cuda(offsets, torch.int32, "offsets")
-    if starts.shape != (b,) or offsets.shape != (b + 1,):
-        raise ValueError("starts must be int32 [%d] and offsets int32 [%d]" % (b, b + 1))
-    pair = ctypes.c_int64 * 2
-    return (k.shape[0], _DTYPES[k.dtype], pair(k.stride(0), k.stride(1)),
-            pair(v.stride(0), v.stride(1)))
+    if starts.dtype is not torch.int32 or offsets.dtype is not torch.int32 or \
+            starts.shape != (b,) or offsets.shape != (b + 1,) or \
+            not starts.is_contiguous() or not offsets.is_contiguous():
+        raise ValueError("starts must be int32 [%d] and offsets int32 [%d], contiguous" % (b, b + 1))
+    _on_device(dev, k, v, starts, offsets)
+    return shape[0], dt, _Strides(ks[0], ks[1]), _Strides(vs[0], vs[1])
 
 
 def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
@@ -610,12 +635,14 @@ def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
     16-byte aligned), sequence b's being offsets[b] .. offsets[b + 1] - 1
     (int32 [B + 1]), written from cache position starts[b] (int32 [B]) on.
     k_cache and v_cache (kv_cache_alloc) are updated in place."""
-    b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache)
-    t, dt, ks, vs = _kv_rows(k, v, cache, starts, offsets)
-    _on_current_device(k, v, starts, offsets, *k_cache, *v_cache)
-    _check(lib.wq_kv_append(_ptr(k), _ptr(v), dt, t, hkv, d, ks, vs, b, _ptr(starts),
-                            _ptr(offsets), cap, *map(_ptr, k_cache), *map(_ptr, v_cache),
-                            _stream(stream)), "wq_kv_append")
+    dev = _current_device()
+    b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
+    t, dt, ks, vs = _kv_rows(k, v, cache, starts, offsets, dev)
+    _check(lib.wq_kv_append(k.data_ptr(), v.data_ptr(), dt, t, hkv, d, ks, vs, b,
+                            starts.data_ptr(), offsets.data_ptr(), cap,
+                            k_cache[0].data_ptr(), k_cache[1].data_ptr(), k_cache[2].data_ptr(),
+                            v_cache[0].data_ptr(), v_cache[1].data_ptr(), v_cache[2].data_ptr(),
+                            _stream_on(dev, stream)), "wq_kv_append")
 
 
 def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k_out=None,
@@ -624,18 +651,20 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
     fp16 or fp32, token t of sequence b (offsets[b] <= t < offsets[b + 1]) from
     cache position starts[b] + t - offsets[b]. Rows behind offsets[B] of a
     given k_out and v_out stay as they were."""
-    b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache)
+    dev = _current_device()
+    b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     if k_out is None:
-        k_out = torch.empty(total, hkv, d, dtype=dtype, device=k_cache[0].device)
+        k_out = torch.empty((total, hkv, d), dtype=dtype, device=k_cache[0].device)
     if v_out is None:
-        v_out = torch.empty(total, hkv, d, dtype=dtype, device=k_cache[0].device)
-    t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets)
+        v_out = torch.empty((total, hkv, d), dtype=dtype, device=k_cache[0].device)
+    t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets, dev)
     if t != total:
         raise ValueError("k_out and v_out must have %d rows" % total)
-    _on_current_device(k_out, v_out, starts, offsets, *k_cache, *v_cache)
-    _check(lib.wq_kv_read(*map(_ptr, k_cache), *map(_ptr, v_cache), b, hkv, d, cap, _ptr(starts),
-                          _ptr(offsets), t, _ptr(k_out), _ptr(v_out), dt, ks, vs,
-                          _stream(stream)), "wq_kv_read")
+    _check(lib.wq_kv_read(k_cache[0].data_ptr(), k_cache[1].data_ptr(), k_cache[2].data_ptr(),
+                          v_cache[0].data_ptr(), v_cache[1].data_ptr(), v_cache[2].data_ptr(),
+                          b, hkv, d, cap, starts.data_ptr(), offsets.data_ptr(), t,
+                          k_out.data_ptr(), v_out.data_ptr(), dt, ks, vs,
+                          _stream_on(dev, stream)), "wq_kv_read")
     return k_out, v_out
 
 
@@ -656,40 +685,43 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
     k_cache and v_cache a cache of B sequences, of which sequence b attends the
     first lengths[b] (int32 [B]) tokens. Returns out [B, Hq, D] of q's type.
     prefix_k = prefix_v = None: no prefix."""
-    if not q.is_cuda or q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("q must be a bfloat16 or float16 CUDA tensor")
-    b, hkv, cap, d = _kv_cache(k_cache, v_cache)
-    if q.dim() != 3 or q.shape[0] != b or q.shape[2] != d:
-        raise ValueError("q must be [%d, Hq, %d], got %s" % (b, d, tuple(q.shape)))
-    hq = q.shape[1]
-    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+    dev = _current_device()
+    b, hkv, cap, d = _kv_cache(k_cache, v_cache, dev)
+    shape, dtype, qs = q.shape, q.dtype, q.stride()
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("q must be bfloat16 or float16, got %s" % dtype)
+    if len(shape) != 3 or shape[0] != b or shape[2] != d:
+        raise ValueError("q must be [%d, Hq, %d], got %s" % (b, d, tuple(shape)))
+    hq = shape[1]
+    if qs[2] != 1 or (hq > 1 and qs[1] != d):
         raise ValueError("the heads of q must be contiguous")
-    _cuda(lengths, torch.int32, "lengths")
-    if lengths.shape != (b,):
-        raise ValueError("lengths must be int32 [%d]" % b)
+    if lengths.dtype is not torch.int32 or lengths.shape != (b,) or not lengths.is_contiguous():
+        raise ValueError("lengths must be int32 [%d], contiguous" % b)
     if prefix_k is None and prefix_v is None:
-        prefix_k = prefix_v = (None, None, None)
+        pre = (None,) * 6
         pcap, prefix_len = 0, 0
     else:
-        one, ph, pcap, pd = _kv_cache(prefix_k, prefix_v)
+        one, ph, pcap, pd = _kv_cache(prefix_k, prefix_v, dev)
         if (one, ph, pd) != (1, hkv, d):
             raise ValueError("the prefix cache must be [1, %d, capacity, ...] with D = %d" % (hkv, d))
-        _on_current_device(*prefix_k, *prefix_v)
         prefix_len = pcap if prefix_len is None else prefix_len
+        pre = (prefix_k[0].data_ptr(), prefix_k[1].data_ptr(), prefix_k[2].data_ptr(),
+               prefix_v[0].data_ptr(), prefix_v[1].data_ptr(), prefix_v[2].data_ptr())
     if workspace is None:
         workspace = prefix_attention_workspace(b, hq, hkv, prefix_len, cap, d, q.device)
     if out is None:
-        out = torch.empty(b, hq, d, dtype=q.dtype, device=q.device)
-    _cuda(out, q.dtype, "out")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    _on_current_device(q, lengths, workspace, out, *k_cache, *v_cache)
-    _check(lib.wq_prefix_attention(_ptr(q), _DTYPES[q.dtype], q.stride(0), b, hq, hkv, d,
-                                   prefix_len, pcap, *map(_ptr, prefix_k), *map(_ptr, prefix_v),
-                                   cap, *map(_ptr, k_cache), *map(_ptr, v_cache), _ptr(lengths),
-                                   _ptr(out), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)),
-           "wq_prefix_attention")
+        out = q.new_empty(shape)
+    elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must have q's type and shape, contiguous")
+    _on_device(dev, q, lengths, workspace, out)
+    _check(lib.wq_prefix_attention(q.data_ptr(), _DTYPES[dtype], qs[0] if b > 1 else hq * d, b, hq,
+                                   hkv, d, prefix_len, pcap, *pre, cap,
+                                   k_cache[0].data_ptr(), k_cache[1].data_ptr(),
+                                   k_cache[2].data_ptr(), v_cache[0].data_ptr(),
+                                   v_cache[1].data_ptr(), v_cache[2].data_ptr(),
+                                   lengths.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(),
+                                   _stream_on(dev, stream)), "wq_prefix_attention")
     return out
 
 

@@ -55,7 +55,7 @@ wq_status read_prefix_error(bool clear, uint32_t* v);
 size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap);
 wq_status launch_prefix_attn(const void*, wq_dtype, int64_t, int64_t, int64_t, int64_t, int64_t,
                              int64_t, const void* const*, int64_t, const void* const*,
-                             const int32_t*, void*, void*, cudaStream_t);
+                             const int32_t*, void*, void*, size_t, cudaStream_t);
 extern std::atomic<int> g_kv_chunks_per_cta;
 wq_status launch_kv_msd(const void*, int64_t, int64_t, int64_t, int64_t, int32_t, const void*,
                         const void*, const void*, const void*, const void*, const void*, void*,
@@ -577,12 +577,9 @@ wq_status wq_prefix_attention(const void* q, wq_dtype dtype, int64_t q_stride, i
   }
   if (!all_aligned({q, out}) || q_stride % 8 != 0) return WQ_ERR_ALIGNMENT;
   if (reinterpret_cast<uintptr_t>(lengths) & 3u) return WQ_ERR_ALIGNMENT;
-  if (!workspace || ws_bytes < prefix_attn_workspace_bytes(B, Hq, Hkv, P, cap))
-    return WQ_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return WQ_ERR_ALIGNMENT;
-  return guarded([&] {
+  return guarded([&] {  // checks the workspace before any launch
     return launch_prefix_attn(q, dtype, q_stride, B, Hq, Hkv, P, prefix_cap, pre, cap, own,
-                              lengths, out, workspace, as_stream(stream));
+                              lengths, out, workspace, ws_bytes, as_stream(stream));
   });
 }
 

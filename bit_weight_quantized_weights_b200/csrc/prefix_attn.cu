@@ -589,13 +589,16 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
     const int64_t tiles = (P + 127) / 128, rt = (rows + 127) / 128;
     pl.tc = rt >= 2 ? 2 : 1;
     pl.nrt = (int)((rt + pl.tc - 1) / pl.tc);
-    int64_t best = INT64_MAX;
-    for (int64_t n = 1; n <= std::min<int64_t>(tiles, 64); ++n) {
-      const int64_t waves = (Hkv * pl.nrt * n + sms - 1) / sms;
-      const int64_t cost = waves * ((tiles + n - 1) / n + 4);
+    // (unit counts beyond 2^30 / 64 fill any number of SMs with one range)
+    const uint32_t units = (uint32_t)std::min<int64_t>(Hkv * pl.nrt, 1 << 24);
+    uint64_t best = UINT64_MAX;
+    for (uint32_t n = 1, most = (uint32_t)std::min<int64_t>(tiles, 64); n <= most; ++n) {
+      const uint32_t waves = (units * n + (uint32_t)sms - 1) / (uint32_t)sms;
+      const uint32_t per = ((uint32_t)tiles + n - 1) / n;
+      const uint64_t cost = (uint64_t)waves * (per + 4);
       if (cost < best) {
         best = cost;
-        pl.chunk_p = (int)((tiles + n - 1) / n) * 128;
+        pl.chunk_p = (int)per * 128;
       }
     }
     pl.ranges = (int)((P + pl.chunk_p - 1) / pl.chunk_p);
@@ -655,16 +658,21 @@ wq_status launch_o(const PrefixArgs& a, const Plan& pl, cudaStream_t st) {
 
 }  // namespace
 
-size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
-  const Plan pl = make_plan(B, Hq, Hkv, P, cap);
+static size_t plan_bytes(const Plan& pl, int64_t B, int64_t Hq) {
   return (size_t)B * Hq * (pl.nsp + pl.nso) * (kD * 4 + 8);
+}
+
+size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
+  return plan_bytes(make_plan(B, Hq, Hkv, P, cap), B, Hq);
 }
 
 wq_status launch_prefix_attn(const void* q, wq_dtype dt, int64_t q_stride, int64_t B, int64_t Hq,
                              int64_t Hkv, int64_t P, int64_t pre_cap, const void* const* pre,
                              int64_t cap, const void* const* own, const int32_t* lengths,
-                             void* out, void* workspace, cudaStream_t st) {
+                             void* out, void* workspace, size_t ws_bytes, cudaStream_t st) {
   const Plan pl = make_plan(B, Hq, Hkv, P, cap);
+  if (!workspace || ws_bytes < plan_bytes(pl, B, Hq)) return WQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WQ_ERR_ALIGNMENT;
   PrefixArgs a;
   a.q = q;
   a.q_stride = q_stride;
