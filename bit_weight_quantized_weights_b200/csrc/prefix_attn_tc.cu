@@ -19,13 +19,13 @@
 // issues (25-27 fill its warpgroup).
 // The operands are the dequantized values themselves, (q - z) s rounded once to
 // fp16 (2^-11), up to a power of two common to 32 keys: a score's scale and the
-// exponent's offset are then one multiply-add for two columns. Exact integers
-// with the scales in a table per key (read by every row) took 12 bytes a column
-// and row group from shared memory, beside the MMAs' operands, and two more
-// operations a weight: 380 us against the present time at 128 sequences x 65537.
-// Within a group of 8 dimensions (K) or keys (V) the nibbles of a code word
-// come out as pairs (0, 4), (1, 5), (2, 6), (3, 7): Q's dimensions and the rows
-// of K (hence the columns of S and P) are stored in that order, 0 4 1 5 2 6 3 7.
+// exponent's offset are then one multiply-add. Exact integers with the scales in
+// a table per key cost 12 bytes of shared memory a column and row, beside the
+// MMAs' operands, and two more operations a weight.
+// Outputs in fp16 (kExact) are eight times finer than in bf16, and there those
+// two roundings would more than double the error: the operands take the leading
+// 7 bits of the scales, which makes them exact, and the rest multiplies the
+// score and the weight, two operations a weight.
 //
 // MMAs of one issuing thread execute in order, so S of a tile completes after
 // the O += P V issued before it: when a softmax warp sees its scores it may
@@ -59,7 +59,7 @@ constexpr int kColO = 256;                 // TMEM columns of the outputs (score
 
 template <int MT>
 constexpr int smem_bytes() {
-  return 1024 + (MT + 4) * kOpBytes + kTabs * 4 * 16 + 256;
+  return 1024 + (MT + 4) * kOpBytes + kTabs * (4 * 16 + kTile / 2 * 8) + 256;
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -68,13 +68,24 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)(127 + x) << 23); }
 
-// fp16 bits of a lane's scale / 2^x, with x (returned) such that the
-// largest of the warp's scales becomes [2^10, 2^11) (a largest below fp16's
-// normal range counts as 2^-14).
+// The scale's leading 7 bits, whose product with q - z (4 bits) is exact in
+// fp16, and what is left of it: s / head - 1 < 2^-6 (2^-15 as bf16).
+__device__ __forceinline__ uint32_t scale_head(uint32_t bits) { return bits & 0xFFF0u; }
+__device__ __forceinline__ float scale_rest(uint32_t bits) {
+  const float h = __half2float(__ushort_as_half((unsigned short)scale_head(bits)));
+  const float s = __half2float(__ushort_as_half((unsigned short)bits));
+  return h > 0.0f ? __fdividef(s - h, h) : 0.0f;
+}
+
+// fp16 bits of a lane's scale (kExact: of its head) / 2^x, with x (returned)
+// such that the largest of the warp's scales becomes [2^10, 2^11) (a largest
+// below fp16's normal range counts as 2^-14).
+template <bool kExact>
 __device__ __forceinline__ uint32_t norm_scale(uint32_t bits, int& x) {
   const uint32_t top = __reduce_max_sync(0xffffffffu, bits & 0x7FFFu);
   x = max((int)(top >> 10), 1) - 25;
-  const float s = __half2float(__ushort_as_half((unsigned short)bits)) * pow2(-x);
+  const uint32_t b = kExact ? scale_head(bits) : bits;
+  const float s = __half2float(__ushort_as_half((unsigned short)b)) * pow2(-x);
   return __half_as_ushort(__float2half_rn(s));
 }
 
@@ -118,7 +129,7 @@ __device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_
                : "memory");
 }
 
-template <int MT>
+template <int MT, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ PrefixArgs p, const WaitCtl wc) {
   extern __shared__ uint8_t smem_raw[];
@@ -129,7 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sv = sk + 2 * kOpBytes;             // [stage]
   // [stage][32 keys]: 2^x of the keys' scales, y of the values', 2^-y
   float4* tab = reinterpret_cast<float4*>(sv + 2 * kOpBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(tab + kTabs * 4);
+  // kExact, [stage][pair of columns]: what the keys' scores and the weights are to
+  // be multiplied with, less 1, as two bf16 each
+  uint2* fac = reinterpret_cast<uint2*>(tab + kTabs * 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(fac + kTabs * (kTile / 2));
   uint64_t* q_full = bars;
   uint64_t* k_full = bars + 1;    // [2]
   uint64_t* k_empty = bars + 3;   // [2]
@@ -181,8 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-    return __all_sync(0xffffffffu, sm100::mbar_wait_hint(bar, parity & 1u, &g_prefix_error, site,
-                                                         abort_flag, wc.limit_ns, 1000));
+    // one suspended poll of up to 20 us covers the waits of a running pipeline
+    return __all_sync(0xffffffffu,
+                      sm100::mbar_try_wait_hint(bar, parity & 1u, 20000) ||
+                          sm100::mbar_wait(bar, parity & 1u, &g_prefix_error, site, abort_flag,
+                                           wc.limit_ns));
   };
 
   if (warp < kSoftWarps) {
@@ -278,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::tc_fence_after();
       const int key_left = end - begin - tile * kTile;
       const float4* tb = tab + (tile % kTabs) * 4;
+      const uint2* fb = fac + (tile % kTabs) * (kTile / 2) + t4;
       uint32_t v[16];
       tmem_ld_16x256b_x4(ts, v);
 #pragma unroll
@@ -289,7 +307,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // pipes only, which the fp16 products of the dequantization need as well;
         // with them the largest batch took 342 us instead of 308)
         float2 t[2][4];  // [row][8 columns: this lane's pair]
+        uint2 d[4];
+        if (kExact)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = fb[16 * c + 4 * j];
         sm100::tmem_ld_wait();
+        if (kExact)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float x = __uint_as_float(v[j]);
+            v[j] = __float_as_uint(fmaf(
+                x, (j & 1) ? bf16_hi_to_f32(d[j >> 2].x) : bf16_lo_to_f32(d[j >> 2].x), x));
+          }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const float cf = crow[n] * sc.x, cm = sc.y - m[n];
@@ -321,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float w0 = ex2(t[n][j].x), w1 = ex2(t[n][j].y);
               e[n].x += w0;
               e[n].y += w1;
-              w[2 * j + n] = pack_f16x2(w0, w1);
+              w[2 * j + n] = kExact ? pack_f16x2(fmaf(w0, bf16_lo_to_f32(d[j].y), w0),
+                                                 fmaf(w1, bf16_hi_to_f32(d[j].y), w1))
+                                    : pack_f16x2(w0, w1);
             }
           }
         };
@@ -511,7 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       // largest to [2^10, 2^11): a product with q - z is at most 30705, and stays
       // a normal fp16 number down to scales 2^-24 of the largest
       int kx, vx;
-      const uint32_t ks = norm_scale(cur[0], kx), vs = norm_scale(cur[2], vx);
+      const uint32_t ks = norm_scale<kExact>(cur[0], kx), vs = norm_scale<kExact>(cur[2], vx);
+      if (kExact && half == 0) {
+        // token 8 j + t is column pair 4 j + t % 4, its first for t < 4
+        uint16_t* at = reinterpret_cast<uint16_t*>(fac + (tile % kTabs) * (kTile / 2) + 16 * w +
+                                                   4 * (lane >> 3) + (lane & 3)) +
+                       ((lane >> 2) & 1);
+        at[0] = bf16_bits(scale_rest(cur[0]));
+        at[2] = bf16_bits(scale_rest(cur[2]));
+      }
       if (lane == 0 && half == 0)
         tab[(tile % kTabs) * 4 + w] = make_float4(pow2(kx), (float)vx, pow2(-vx), 0.0f);
 #pragma unroll
@@ -666,21 +705,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kIssueWarp) sm100::tmem_dealloc(tmem, 512);
 }
 
-template <int MT>
+template <int MT, bool kExact>
 wq_status launch(const PrefixArgs& a, cudaStream_t st) {
   static bool attr_set = [] {
-    return cudaFuncSetAttribute(prefix_tc_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(prefix_tc_kernel<MT, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 smem_bytes<MT>()) == cudaSuccess;
   }();
   if (!attr_set) return WQ_ERR_CUDA;
-  prefix_tc_kernel<MT><<<(unsigned)a.nprefix, kThreads, smem_bytes<MT>(), st>>>(a, wait_ctl());
+  prefix_tc_kernel<MT, kExact><<<(unsigned)a.nprefix, kThreads, smem_bytes<MT>(), st>>>(a, wait_ctl());
   return launch_status();
 }
 
 }  // namespace
 
 wq_status launch_prefix_tc(const PrefixArgs& a, int row_tiles, cudaStream_t st) {
-  return row_tiles == 2 ? launch<2>(a, st) : launch<1>(a, st);
+  if (a.fp16) return row_tiles == 2 ? launch<2, true>(a, st) : launch<1, true>(a, st);
+  return row_tiles == 2 ? launch<2, false>(a, st) : launch<1, false>(a, st);
 }
 
 wq_status read_prefix_error(bool clear, uint32_t* v) {
