@@ -578,7 +578,7 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
     n = (int)((keys + chunk - 1) / chunk);
   };
   pl.nto = R <= 8 ? 1 : 2;
-  pl.ntp = rows <= 8 ? 1 : 2;
+  pl.ntp = rows <= 8 || P == 0 ? 1 : 2;
   pl.tc = 0;
   pl.nsp = pl.ranges = 0;
   pl.nrt = 0;
