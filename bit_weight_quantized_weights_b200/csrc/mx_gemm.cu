@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 // multiplied with every plane's token tile. A stage holds 256 k (128-byte rows
 // of 4-bit codes, 128-byte swizzle) of all operands.
 //   warp 0       TMA loads of the codes
-//   warp 1       tcgen05.mma: the whole warp runs the loop and one elected lane
+//   warps 1, 2   tcgen05.mma: the whole warp runs the loop and one elected lane
 //                issues, so that the operands' addresses are warp-uniform (a
 //                loop of one lane spent 90 cycles an MMA moving them to the
 //                uniform registers the instruction takes: 1100 cycles a stage)
@@ -240,7 +240,13 @@ struct MxCfg {
   // stages whose scales are on their way in registers (32 registers a stage at
   // most): one stage ahead cost 0.55 us a stage, the latency of the loads
   static constexpr int kSfAhead = BN >= 256 ? 2 : 3;
-  static constexpr int kCols = BN + kStages * kSfCols;
+  // Warps that issue MMAs. Issuing a stage (the wait, 4 or 8 MMAs, the commit)
+  // takes 650 cycles, more than the MMAs of tiles up to 128 wide: two warps
+  // then take the stages in turn, each with an accumulator of its own, which
+  // the epilogue adds.
+  static constexpr int kIssuers = BN <= 128 ? 2 : 1;
+  static constexpr int kAccCols = kIssuers * BN;
+  static constexpr int kCols = kAccCols + kStages * kSfCols;
   static constexpr int kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "TMEM columns");
 };
@@ -312,9 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&empty[s], 1);
       sm100::mbar_init(&sffull[s], 4);
     }
-    sm100::mbar_init(acc_full, 1);
+    sm100::mbar_init(acc_full, Cfg::kIssuers);
     sm100::mbar_init(acc_empty, Cfg::kEpiWarps);
-    sm100::mbar_init(mma_done, 1);
+    sm100::mbar_init(mma_done, Cfg::kIssuers);
     *abort_flag = 0;
     sm100::fence_mbar_init();
   }
@@ -326,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tmem_sf = tmem + BN;
+  const uint32_t tmem_sf = tmem + Cfg::kAccCols;
 
   int last_issued = -1;
   if (warp == 0) {
@@ -356,12 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else if (warp == 1) {
-    const uint32_t xlo0 = sm100::uniform(sm100::sdesc_lo(smem_u32(sx))), wlo0 = sm100::uniform(sm100::sdesc_lo(smem_u32(sw)));
-    const uint32_t tm = sm100::uniform(tmem);
-    int it = 0, n = 0;
+  } else if (warp <= Cfg::kIssuers) {
+    const int who = warp - 1;
+    const uint32_t xlo0 = sm100::uniform(sm100::sdesc_lo(smem_u32(sx)));
+    const uint32_t wlo0 = sm100::uniform(sm100::sdesc_lo(smem_u32(sw)));
+    const uint32_t tm = sm100::uniform(tmem), acc = tm + (uint32_t)(who * BN);
+    int it0 = 0, n = 0;  // the tile's first stage; the tile
     bool ok = true;
-    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n) {
+    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n, it0 += KT) {
       if (n > 0) {
         ok = __all_sync(0xffffffffu,
                         sm100::mbar_wait(acc_empty, (uint32_t)(n - 1) & 1u, &g_mx_gemm_error,
@@ -369,8 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         sm100::tc_fence_after();
       }
-      for (int kt = 0; kt < KT; ++kt, ++it) {
-        const int s = it % S;
+      for (int kt = who; kt < KT; kt += Cfg::kIssuers) {
+        const int it = it0 + kt, s = it % S;
         const uint32_t ph = (uint32_t)(it / S) & 1u;
         ok = __all_sync(0xffffffffu, sm100::mbar_wait(&full[s], ph, &g_mx_gemm_error, 0x3202u,
                                                       abort_flag, wc.limit_ns) &&
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                           0x3203u, abort_flag, wc.limit_ns));
         if (!ok) break;
         sm100::tc_fence_after();
-        const uint32_t sf = tm + BN + (uint32_t)(s * Cfg::kSfCols);
+        const uint32_t sf = tm + Cfg::kAccCols + (uint32_t)(s * Cfg::kSfCols);
         const uint32_t xlo = xlo0 + (uint32_t)(s * (Cfg::kXBytes >> 4));
         const uint32_t wlo = wlo0 + (uint32_t)(s * (Cfg::kWBytes >> 4));
         if (sm100::elect_one()) {
@@ -389,15 +397,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sfb = sf + PL * 8 + kg * 4 * Cfg::kWPieces;
 #pragma unroll
             for (int p = 0; p < PL; ++p)
-              mma_mxf4(tm, sm100::sdesc_at(xlo + p * (kBM * kBKBytes >> 4) + kk * 2),
+              mma_mxf4(acc, sm100::sdesc_at(xlo + p * (kBM * kBKBytes >> 4) + kk * 2),
                        sm100::sdesc_at(wlo + kk * 2), idesc, sf + (p * 2 + kg) * 4, sfb,
-                       (kk | p) != 0 || kt != 0 ? 1u : 0u);
+                       (kk | p) != 0 || kt != who ? 1u : 0u);
           }
           sm100::mma_commit(&empty[s]);
-          if (kt == KT - 1) sm100::mma_commit(acc_full);
         }
         __syncwarp();
       }
+      if (ok && sm100::elect_one()) sm100::mma_commit(acc_full);
+      __syncwarp();
     }
     if (sm100::elect_one()) sm100::mma_commit(mma_done);
     __syncwarp();
@@ -504,6 +513,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[32];
         sm100::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + part * kCols + 32 * c, v);
         sm100::tmem_ld_wait();
+        if (Cfg::kIssuers == 2 && KT > 1) {
+          uint32_t u[32];
+          sm100::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + BN + part * kCols + 32 * c, u);
+          sm100::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           out[16 * c + j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
