@@ -472,7 +472,8 @@ wq_status wq_mx_quantize_planes(const void* x, wq_dtype dtype, int64_t ldx, int6
   if (!x || !codes || !scales) return WQ_ERR_INVALID_ARG;
   if (!all_aligned({x, codes, scales}) || ldx % (dtype == WQ_FP32 ? 4 : 8) != 0)
     return WQ_ERR_ALIGNMENT;
-  if (M > INT32_MAX || K > INT32_MAX - 255) return WQ_ERR_UNSUPPORTED;
+  if (M > INT32_MAX || K > INT32_MAX - 511 || M * ((K + 511) / 512) > INT32_MAX)
+    return WQ_ERR_UNSUPPORTED;
   return guarded([&] {
     return launch_mx_planes(x, dtype, ldx, M, K, n_planes, codes, scales, as_stream(stream));
   });

@@ -22,9 +22,9 @@ __device__ unsigned int g_mx_gemm_error;
 namespace {
 
 // ---------------------------------------------------------------------------
-// Quantization of activations: one warp takes 256 consecutive elements of a
-// row, 8 elements a lane, so a block of 32 is 4 lanes (two shuffles for its
-// largest magnitude) and a lane's codes are one 32-bit store.
+// Quantization of activations: one warp takes 512 consecutive elements of a
+// row, 16 elements a lane, so a block of 32 is two lanes (one shuffle for its
+// largest magnitude) and a lane's codes are one 64-bit store.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float pow2f(int e) {  // exact for e in [-127, 127]
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(0x00400000u);
@@ -42,7 +42,7 @@ __device__ __forceinline__ int e2m1_exponent(float a) {
 
 // Eight E2M1 codes of f[i] * scale, element i in nibble i (a negative value
 // that rounds to zero has code 8 here).
-__device__ __forceinline__ uint32_t e2m1_x8(const float (&f)[8], float scale) {
+__device__ __forceinline__ uint32_t e2m1_x8(const float* f, float scale) {
   uint32_t w;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -83,35 +83,36 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, float (&v)[8]) {
   }
 }
 
+// 16 consecutive elements.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 v = ld_stream_u4(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void load16(const T* p, float (&f)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo_to_f32(w[i]);
-    f[2 * i + 1] = bf16_hi_to_f32(w[i]);
+  for (int h = 0; h < 2; ++h) {
+    const uint4 v = ld_stream_u4(p + 8 * h);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
+        f[8 * h + 2 * i] = bf16_lo_to_f32(w[i]);
+        f[8 * h + 2 * i + 1] = bf16_hi_to_f32(w[i]);
+      } else {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[8 * h + 2 * i] = t.x;
+        f[8 * h + 2 * i + 1] = t.y;
+      }
+    }
   }
 }
 template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&f)[8]) {
-  const uint4 v = ld_stream_u4(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void load16<float>(const float* p, float (&f)[16]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
+  for (int h = 0; h < 4; ++h) {
+    const uint4 v = ld_stream_u4(p + 4 * h);
+    f[4 * h] = __uint_as_float(v.x);
+    f[4 * h + 1] = __uint_as_float(v.y);
+    f[4 * h + 2] = __uint_as_float(v.z);
+    f[4 * h + 3] = __uint_as_float(v.w);
   }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
-  const uint4 a = ld_stream_u4(p), b = ld_stream_u4(p + 4);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
 }
 
 template <typename T, int PL>
@@ -119,35 +120,47 @@ __global__ void __launch_bounds__(256)
     mx_planes_kernel(const T* __restrict__ x, int64_t ldx, int M, int K,
                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
-  const int chunks = (K + 255) / 256;
-  const int64_t total = (int64_t)M * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total;
-       i += (int64_t)gridDim.x * 8) {
-    const int m = (int)(i / chunks);
-    const int k = (int)(i - (int64_t)m * chunks) * 256 + 8 * lane;
+  const uint32_t chunks = (uint32_t)(K + 511) / 512;
+  const uint32_t total = (uint32_t)M * chunks;  // below 2^31
+  for (uint32_t i = blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += gridDim.x * 8) {
+    const uint32_t m = i / chunks;
+    const int k = (int)(i - m * chunks) * 512 + 16 * lane;
     const bool in = k < K;  // whole blocks: K is a multiple of 32
-    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (in) load8(x + (int64_t)m * ldx + k, f);
+    float f[16];
+    if (in) {
+      load16(x + (int64_t)m * ldx + k, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+    }
 #pragma unroll
     for (int p = 0; p < PL; ++p) {
-      float a = 0.0f;
+      float a = 0.0f, b = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
+      for (int j = 0; j < 8; ++j) {
+        a = fmaxf(a, fabsf(f[j]));
+        b = fmaxf(b, fabsf(f[8 + j]));
+      }
+      a = fmaxf(a, b);
       a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
       const int e = e2m1_exponent(a);
-      const uint32_t w = e2m1_x8(f, pow2f(-e));
+      const float down = pow2f(-e);
+      const uint32_t w[2] = {e2m1_x8(f, down), e2m1_x8(f + 8, down)};
       if (in) {
         const int64_t row = (int64_t)p * M + m;
-        *reinterpret_cast<uint32_t*>(codes + (row * K + k) / 2) = plus_zero(w);
-        if ((lane & 3) == 0) scales[(row * K + k) / 32] = (uint8_t)(e + 127);
+        *reinterpret_cast<uint2*>(codes + (row * K + k) / 2) =
+            make_uint2(plus_zero(w[0]), plus_zero(w[1]));
+        if ((lane & 1) == 0) scales[(row * K + k) / 32] = (uint8_t)(e + 127);
       }
       if (p + 1 < PL) {
         const float up = pow2f(e);
-        float v[8];
-        e2m1_values(w, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = fmaf(-v[j], up, f[j]);  // exact
+        for (int h = 0; h < 2; ++h) {
+          float v[8];
+          e2m1_values(w[h], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[8 * h + j] = fmaf(-v[j], up, f[8 * h + j]);  // exact
+        }
       }
     }
   }
@@ -622,7 +635,7 @@ wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const 
 template <typename T>
 void planes(const void* x, int64_t ldx, int M, int K, int P, uint8_t* codes, uint8_t* scales,
             cudaStream_t st) {
-  const int64_t total = (int64_t)M * ((K + 255) / 256);
+  const int64_t total = (int64_t)M * ((K + 511) / 512);
   const unsigned grid = (unsigned)std::min<int64_t>((total + 7) / 8, (int64_t)num_sms() * 64);
   if (P == 1)
     mx_planes_kernel<T, 1><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, M, K, codes, scales);
