@@ -44,23 +44,6 @@ struct KvRows {            // packed rows and where they belong
   int nblk;                // ceil(cap / 8)
 };
 
-// 32-way search: the last b in [0, B) whose first unit offsets[b] / 8 + 2 b is
-// at most u (0 if there is none).
-__device__ __forceinline__ int find_seq(const int32_t* offsets, int B, int64_t u, int lane) {
-  int lo = 0, n = B;
-  while (n > 1) {
-    const int step = (n + 31) >> 5;
-    const int i = lane * step;
-    const bool in = i < n;
-    const int64_t first = in ? (int64_t)(offsets[lo + i] >> 3) + 2 * (int64_t)(lo + i) : 0;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, in && first <= u));
-    const int skip = (cnt > 0 ? cnt - 1 : 0) * step;
-    lo += skip;
-    n = min(step, n - skip);
-  }
-  return lo;
-}
-
 // What a warp works on: block `blk` of sequence b and, for its lane's half,
 // the token index of each of its 4 rows (-1: not written or read).
 struct Unit {
@@ -70,12 +53,33 @@ struct Unit {
   bool any;
 };
 
+// 32-way search for the last b in [0, B) whose first unit offsets[b] / 8 + 2 b
+// is at most u (0 if there is none). The last round loads what the found
+// sequence needs with its keys, so that up to 32 sequences take one round of
+// loads in all.
 __device__ __forceinline__ Unit find_unit(const KvRows& p, int64_t u, int half, int lane,
                                           bool clip) {
+  int lo = 0, n = p.B;
+  while (n > 32) {
+    const int step = (n + 31) >> 5;
+    const int i = lane * step;
+    const bool in = i < n;
+    const int64_t first = in ? (int64_t)(p.offsets[lo + i] >> 3) + 2 * (int64_t)(lo + i) : 0;
+    const int cnt = __popc(__ballot_sync(0xffffffffu, in && first <= u));
+    const int skip = (cnt > 0 ? cnt - 1 : 0) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  const bool in = lane < n;
+  const int32_t o0 = in ? p.offsets[lo + lane] : 0, o1 = in ? p.offsets[lo + lane + 1] : 0;
+  const int32_t s0 = in ? p.starts[lo + lane] : 0;
+  const int cnt = __popc(__ballot_sync(
+      0xffffffffu, in && (int64_t)(o0 >> 3) + 2 * (int64_t)(lo + lane) <= u));
+  const int at = cnt > 0 ? cnt - 1 : 0;
   Unit w;
-  w.b = find_seq(p.offsets, p.B, u, lane);
-  const int64_t t0 = p.offsets[w.b], t1 = p.offsets[w.b + 1];
-  const int64_t first = p.starts[w.b];
+  w.b = lo + at;
+  const int64_t t0 = __shfl_sync(0xffffffffu, o0, at), t1 = __shfl_sync(0xffffffffu, o1, at);
+  const int64_t first = __shfl_sync(0xffffffffu, s0, at);
   const int64_t local = u - ((t0 >> 3) + 2 * (int64_t)w.b);
   w.blk = (first >> 3) + local;
   w.any = local >= 0 && 8 * w.blk < first + (t1 - t0);
@@ -159,10 +163,12 @@ __device__ __forceinline__ float div_by(float a, float b, float y) {
   return __fmaf_rn(__fmaf_rn(-q, b, a), y, q);
 }
 
-// One group of 16 lanes x 8 elements: codes (0..15), scale and zero.
-__device__ __forceinline__ void quantize_row(const float (&f)[8], uint32_t (&c)[8], __half& sh,
-                                             int& z) {
-  float lo = 0.0f, hi = 0.0f;
+// min(0, min x) and max(0, max x) of a row: 16 lanes x 8 elements. 16-bit types
+// keep (min, -max) packed in one register: a packed minimum and a shuffle a step.
+__device__ __forceinline__ void row_range(const Row<float>& r, float& lo, float& hi) {
+  float f[8];
+  r.get(f);
+  lo = hi = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     lo = fminf(lo, f[i]);
@@ -173,26 +179,60 @@ __device__ __forceinline__ void quantize_row(const float (&f)[8], uint32_t (&c)[
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
-  sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
+}
+template <typename P>  // a packed pair type
+__device__ __forceinline__ P min2(P a, P b) { return __hmin2(a, b); }
+template <typename P, typename T>
+__device__ __forceinline__ uint32_t packed_range(const Row<T>& r) {
+  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+  auto as = [](uint32_t u) { return *reinterpret_cast<P*>(&u); };
+  auto bits = [](P v) { return *reinterpret_cast<uint32_t*>(&v); };
+  constexpr uint32_t kNeg = 0x80008000u;
+  const P n = min2(min2(as(w[0]), as(w[1])), min2(as(w[2]), as(w[3])));
+  const P x = min2(min2(as(w[0] ^ kNeg), as(w[1] ^ kNeg)),
+                   min2(as(w[2] ^ kNeg), as(w[3] ^ kNeg)));
+  P m = min2(as(prmt(bits(n), bits(x), 0x5410)), as(prmt(bits(n), bits(x), 0x7632)));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1)
+    m = min2(m, as(__shfl_xor_sync(0xffffffffu, bits(m), o)));
+  return bits(m);
+}
+__device__ __forceinline__ void row_range(const Row<__nv_bfloat16>& r, float& lo, float& hi) {
+  const uint32_t m = packed_range<__nv_bfloat162>(r);
+  lo = fminf(0.0f, bf16_lo_to_f32(m));
+  hi = fmaxf(0.0f, -bf16_hi_to_f32(m));
+}
+__device__ __forceinline__ void row_range(const Row<__half>& r, float& lo, float& hi) {
+  const uint32_t m = packed_range<__half2>(r);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+  lo = fminf(0.0f, f.x);
+  hi = fmaxf(0.0f, -f.y);
+}
+
+// rint(v) + z clamped to 0 .. 15, for |v| far below 2^22 (here at most about
+// 30: fp16's smallest scales are off by at most half of themselves): adding
+// 1.5 * 2^23 leaves the integer in the low mantissa bits; the integer sum and
+// both bounds are one instruction.
+__device__ __forceinline__ int code_of(float v, int z) {
+  return __viaddmin_s32_relu(__float_as_int(__fadd_rn(v, 12582912.0f)), z - 0x4B400000, 15);
+}
+
+// Scale, its reciprocal and the zero of a row's range.
+__device__ __forceinline__ void row_scale(float lo, float hi, __half& sh, float& s, float& y,
+                                          int& z) {
+  // (hi - lo) / 15 rounded to nearest
+  sh = __float2half_rn(div_by(__fsub_rn(hi, lo), 15.0f, 1.0f / 15.0f));
   if (__half2float(sh) == 0.0f) {  // an all-zero (or vanishing) row: range [-1, 1]
     lo = -1.0f;
-    sh = __float2half_rn(__fdiv_rn(2.0f, 15.0f));
+    sh = __float2half_rn(2.0f / 15.0f);
   }
-  const float s = __half2float(sh);
-  const float y = __frcp_rn(s);
-  z = (int)fminf(fmaxf(rintf(div_by(-lo, s, y)), 0.0f), 15.0f);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // rint(x / s) by adding 1.5 * 2^23 (|x / s| <= 30: fp16's smallest scales
-    // are off by at most half of themselves)
-    const float r = __fadd_rn(div_by(f[i], s, y), 12582912.0f);
-    const int q = (int)(__float_as_uint(r) - 0x4B400000u) + z;
-    c[i] = (uint32_t)min(max(q, 0), 15);
-  }
+  s = __half2float(sh);
+  y = __frcp_rn(s);
+  z = code_of(div_by(-lo, s, y), 0);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
     kv_append_kernel(KvRows p, const T* __restrict__ k, const T* __restrict__ v,
                      uint32_t* __restrict__ kc, __half* __restrict__ ks, __half* __restrict__ kz,
                      uint32_t* __restrict__ vc, __half* __restrict__ vs,
@@ -228,46 +268,55 @@ __global__ void __launch_bounds__(256)
   uint4 old = make_uint4(0, 0, 0, 0);
   if (mask != 0xFFu) old = *vword;
 
-  // rows r = 0..3 of this half are block positions 2 r + half
-  __half s_k = __float2half(0.0f), s_v = s_k, z_k = s_k, z_v = s_k;
-  uint32_t words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  // Rows r = 0..3 of this half are block positions 2 r + half. The ranges of its
+  // 4 K and 4 V rows first: lane r (K) or 4 + r (V) of the half then works out
+  // that row's scale, once for the row instead of once a lane.
+  float mylo = 0.0f, myhi = 0.0f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     // bits 2 r and 2 r + 1: either half has a row (the shuffles take both)
     if (((mask >> (2 * r)) & 3u) == 0) continue;
-    float f[8];
-    uint32_t c[8];
-    __half s;
-    int z;
-    kr[r].get(f);
-    quantize_row(f, c, s, z);
-    if (w.tok[r] >= 0) {
-      uint32_t word = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) word |= c[i] << (4 * i);
-      kc[(row0 + 2 * r + half) * (kD / 8) + col] = word;
-    }
-    if (col == r) {
-      s_k = s;
-      z_k = __int2half_rn(z);
-    }
-    vr[r].get(f);
-    quantize_row(f, c, s, z);
-    const int sh = 4 * (2 * r + half);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) words[i] |= c[i] << sh;
-    if (col == r) {
-      s_v = s;
-      z_v = __int2half_rn(z);
-    }
+    float lo, hi;
+    row_range(kr[r], lo, hi);
+    if (col == r) mylo = lo, myhi = hi;
+    row_range(vr[r], lo, hi);
+    if (col == 4 + r) mylo = lo, myhi = hi;
   }
-  // lane col (< 4) holds row col's scales: one store an array covers the block
-  if (col < 4 && ((mask >> (2 * col + half)) & 1u)) {
-    const int64_t at = row0 + 2 * col + half;
-    ks[at] = s_k;
-    kz[at] = z_k;
-    vs[at] = s_v;
-    vz[at] = z_v;
+  __half sh;
+  float s, y;
+  int z;
+  row_scale(mylo, myhi, sh, s, y, z);
+  uint32_t words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    if (((mask >> (2 * r)) & 3u) == 0) continue;
+    float f[8];
+    int from = 16 * half + r;
+    float sr = __shfl_sync(0xffffffffu, s, from), yr = __shfl_sync(0xffffffffu, y, from);
+    int zr = __shfl_sync(0xffffffffu, z, from);
+    kr[r].get(f);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      word |= (uint32_t)code_of(div_by(f[i], sr, yr), zr) << (4 * i);
+    if (w.tok[r] >= 0) kc[(row0 + 2 * r + half) * (kD / 8) + col] = word;
+    from += 4;
+    sr = __shfl_sync(0xffffffffu, s, from);
+    yr = __shfl_sync(0xffffffffu, y, from);
+    zr = __shfl_sync(0xffffffffu, z, from);
+    vr[r].get(f);
+    const int bit = 4 * (2 * r + half);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      words[i] |= (uint32_t)code_of(div_by(f[i], sr, yr), zr) << bit;
+  }
+  {
+    const int r = col & 3;
+    if (col < 8 && ((mask >> (2 * r + half)) & 1u)) {
+      const int64_t at = row0 + 2 * r + half;
+      (col < 4 ? ks : vs)[at] = sh;
+      (col < 4 ? kz : vz)[at] = __int2half_rn(z);
+    }
   }
   // the two halves hold the even and the odd positions of the same 8 words:
   // each keeps 4 of them
@@ -300,7 +349,7 @@ __device__ __forceinline__ float code_value(uint32_t w, int sh, float zb, float 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
     kv_read_kernel(KvRows p, const uint32_t* __restrict__ kc, const __half* __restrict__ ks,
                    const __half* __restrict__ kz, const uint32_t* __restrict__ vc,
                    const __half* __restrict__ vs, const __half* __restrict__ vz,

@@ -83,3 +83,42 @@ def test_prefix_attention_validation(wq):
                                                 ctypes.byref(size)) == wq.WQ_ERR_UNSUPPORTED
     assert wq.lib.wq_prefix_attention_workspace(2, 8, 2, 128, 24, 16, None) == \
         wq.WQ_ERR_INVALID_ARG
+
+
+def _planes(wq, x=A16, dt=0, ldx=512, m=4, k=512, n=2, c=A16, s=A16):
+    return wq.lib.wq_mx_quantize_planes(x, dt, ldx, m, k, n, c, s, None)
+
+
+def test_mx_planes_validation(wq):
+    assert _planes(wq, m=0) == wq.WQ_OK
+    for bad in (dict(m=-1), dict(k=0), dict(k=48), dict(ldx=504), dict(n=0), dict(n=3), dict(dt=3),
+                dict(x=None), dict(c=None), dict(s=None)):
+        assert _planes(wq, **bad) == wq.WQ_ERR_INVALID_ARG, bad
+    for bad in (dict(x=MIS), dict(c=MIS), dict(s=MIS), dict(ldx=516), dict(dt=2, ldx=514)):
+        assert _planes(wq, **bad) == wq.WQ_ERR_ALIGNMENT, bad
+    for bad in (dict(m=2 ** 31), dict(m=2 ** 30, k=2048, ldx=2048)):
+        assert _planes(wq, **bad) == wq.WQ_ERR_UNSUPPORTED, bad
+
+
+def _gemm(wq, c=A16, s=A16, m=4, n=256, k=512, p=2, wc=A16, ws=A16, y=A16, w=A16, size=1 << 40):
+    return wq.lib.wq_mx_gemm(c, s, m, n, k, p, wc, ws, y, w, size, None)
+
+
+def test_mx_gemm_validation(wq):
+    assert _gemm(wq, m=0) == wq.WQ_OK
+    assert _gemm(wq, n=0) == wq.WQ_OK
+    for bad in (dict(m=-1), dict(n=-1), dict(k=0), dict(k=48), dict(p=0), dict(p=3), dict(c=None),
+                dict(s=None), dict(wc=None), dict(ws=None), dict(y=None)):
+        assert _gemm(wq, **bad) == wq.WQ_ERR_INVALID_ARG, bad
+    for bad in (dict(c=MIS), dict(s=MIS), dict(wc=MIS), dict(ws=MIS), dict(y=MIS), dict(w=MIS)):
+        assert _gemm(wq, **bad) == wq.WQ_ERR_ALIGNMENT, bad
+    for bad in (dict(k=96), dict(n=24), dict(m=2 ** 30), dict(n=2 ** 31), dict(k=2 ** 31),
+                dict(m=2 ** 29, n=2 ** 20)):
+        assert _gemm(wq, **bad) == wq.WQ_ERR_UNSUPPORTED, bad
+    need = wq.wq_workspace_bytes(wq.WQ_OP_MX_GEMM, 4, 256, 512, 0, 2)
+    assert need > 0
+    assert _gemm(wq, w=None) == wq.WQ_ERR_WORKSPACE
+    assert _gemm(wq, size=need - 1) == wq.WQ_ERR_WORKSPACE
+    assert wq.wq_workspace_bytes(wq.WQ_OP_MX_GEMM, 0, 256, 512, 0, 2) == 0
+    with pytest.raises(wq.WqError):
+        wq.wq_workspace_bytes(wq.WQ_OP_MX_GEMM, 4, 256, 512, 0, 3)
