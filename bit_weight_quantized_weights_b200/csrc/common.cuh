@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/wq.h"
 
 #if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ < 1000)
@@ -54,6 +56,22 @@ inline int num_sms() {
     return n;
   }();
   return sms;
+}
+
+// Allow `kernel` `bytes` of dynamic shared memory on the current device. The
+// attribute belongs to a device: `done`, one per kernel, has a bit for each of
+// the first 64 (later ones are set at every call).
+template <typename F>
+inline bool allow_smem(F kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 // ---------------------------------------------------------------------------

@@ -593,11 +593,8 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, cons
   if (!make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, wcodes, (uint64_t)a0.K / 2,
                     (uint64_t)a0.N, (uint64_t)a0.K / 2, kBKBytes, BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return WQ_ERR_CUDA;
-  static bool attr_set = [] {
-    return cudaFuncSetAttribute(mx_gemm_kernel<BN, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg::kSmem) == cudaSuccess;
-  }();
-  if (!attr_set) return WQ_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!allow_smem(mx_gemm_kernel<BN, PL>, Cfg::kSmem, smem_set)) return WQ_ERR_CUDA;
   MxArgs a = a0;
   a.tiles = a.mt * ((a.N + BN - 1) / BN);
   cudaLaunchConfig_t cfg = {};

@@ -589,10 +589,12 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
     const int64_t tiles = (P + 127) / 128, rt = (rows + 127) / 128;
     pl.tc = rt >= 2 ? 2 : 1;
     pl.nrt = (int)((rt + pl.tc - 1) / pl.tc);
-    // (unit counts beyond 2^30 / 64 fill any number of SMs with one range)
+    // (about two waves at most; 2^24 units fill any number of SMs with one range)
     const uint32_t units = (uint32_t)std::min<int64_t>(Hkv * pl.nrt, 1 << 24);
     uint64_t best = UINT64_MAX;
-    for (uint32_t n = 1, most = (uint32_t)std::min<int64_t>(tiles, 64); n <= most; ++n) {
+    const uint32_t most = (uint32_t)std::min<int64_t>(
+        tiles, std::max<uint32_t>(8, 2 * (uint32_t)sms / units + 1));
+    for (uint32_t n = 1; n <= most; ++n) {
       const uint32_t waves = (units * n + (uint32_t)sms - 1) / (uint32_t)sms;
       const uint32_t per = ((uint32_t)tiles + n - 1) / n;
       const uint64_t cost = (uint64_t)waves * (per + 4);
@@ -627,11 +629,8 @@ wq_status launch(const PrefixArgs& a, int tc, cudaStream_t st) {
   }
   const int nprefix = tc ? 0 : a.nprefix;
   constexpr int kSmem = attn_smem<(NTP > NTO ? NTP : NTO)>();
-  static bool attr_set = [] {
-    return cudaFuncSetAttribute(prefix_attn_kernel<NTP, NTO>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess;
-  }();
-  if (!attr_set) return WQ_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!allow_smem(prefix_attn_kernel<NTP, NTO>, kSmem, smem_set)) return WQ_ERR_CUDA;
   cfg.gridDim = dim3((unsigned)(nprefix + (int64_t)a.nso * a.Hkv * a.B), 1, 1);
   cfg.blockDim = dim3(32 * kWarps, 1, 1);
   cfg.dynamicSmemBytes = kSmem;

@@ -707,11 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int MT, bool kExact>
 wq_status launch(const PrefixArgs& a, cudaStream_t st) {
-  static bool attr_set = [] {
-    return cudaFuncSetAttribute(prefix_tc_kernel<MT, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem_bytes<MT>()) == cudaSuccess;
-  }();
-  if (!attr_set) return WQ_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!allow_smem(prefix_tc_kernel<MT, kExact>, smem_bytes<MT>(), smem_set)) return WQ_ERR_CUDA;
   prefix_tc_kernel<MT, kExact><<<(unsigned)a.nprefix, kThreads, smem_bytes<MT>(), st>>>(a, wait_ctl());
   return launch_status();
 }
