@@ -45,6 +45,7 @@ EXPORTED = [
     "wq_msd_decode_attention", "wq_msd_decode_attention_workspace",
     "wq_test_set_attention_split", "wq_kv_block_values", "wq_kv_append", "wq_kv_read",
     "wq_prefix_attention", "wq_prefix_attention_workspace", "wq_mx_quantize_planes", "wq_mx_gemm",
+    "wq_test_set_prefix_path",
 ]
 
 _DTYPES = {torch.bfloat16: WQ_BF16, torch.float16: WQ_FP16, torch.float32: WQ_FP32}
@@ -92,6 +93,7 @@ def _load():
         "wq_msd_decode_attention_workspace": ([I64, I64, I64, I64, I32, I32, ctypes.POINTER(SZ)],
                                               ctypes.c_int),
         "wq_test_set_attention_split": ([I32], ctypes.c_int),
+        "wq_test_set_prefix_path": ([I32], ctypes.c_int),
         "wq_kv_block_values": ([P, I64, I64, I32, P, P], ctypes.c_int),
         "wq_kv_append": ([P, P, ctypes.c_int, I64, I64, I32, ctypes.POINTER(I64),
                           ctypes.POINTER(I64), I64, P, P, I64, P, P, P, P, P, P, P], ctypes.c_int),
@@ -766,3 +768,8 @@ def wq_msd_decode_attention(q, k_cache, v_cache, n_components=2, workspace=None,
 def wq_test_set_attention_split(chunks_per_cta=0):
     """Fix the attention kernel's chunks per CTA (0: chosen per launch)."""
     _check(lib.wq_test_set_attention_split(chunks_per_cta), "wq_test_set_attention_split")
+
+
+def wq_test_set_prefix_path(path=0):
+    """Fix the kernel that takes the prefix (0: chosen per call, 1: mma.sync, 2: tcgen05)."""
+    _check(lib.wq_test_set_prefix_path(path), "wq_test_set_prefix_path")

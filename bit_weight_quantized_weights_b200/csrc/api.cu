@@ -56,6 +56,7 @@ size_t prefix_attn_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t P
 wq_status launch_prefix_attn(const void*, wq_dtype, int64_t, int64_t, int64_t, int64_t, int64_t,
                              int64_t, const void* const*, int64_t, const void* const*,
                              const int32_t*, void*, void*, size_t, cudaStream_t);
+extern std::atomic<int> g_prefix_path;
 extern std::atomic<int> g_kv_chunks_per_cta;
 wq_status launch_kv_msd(const void*, int64_t, int64_t, int64_t, int64_t, int32_t, const void*,
                         const void*, const void*, const void*, const void*, const void*, void*,
@@ -651,6 +652,12 @@ wq_status wq_test_set_wait(uint64_t limit_ns, int stall) {
 wq_status wq_test_set_attention_split(int32_t chunks_per_cta) {
   if (chunks_per_cta < 0 || chunks_per_cta > 64) return WQ_ERR_INVALID_ARG;
   g_kv_chunks_per_cta.store(chunks_per_cta, std::memory_order_relaxed);
+  return WQ_OK;
+}
+
+wq_status wq_test_set_prefix_path(int32_t path) {
+  if (path < 0 || path > 2) return WQ_ERR_INVALID_ARG;
+  g_prefix_path.store(path, std::memory_order_relaxed);
   return WQ_OK;
 }
 

@@ -28,6 +28,8 @@ namespace wq {
 
 wq_status launch_prefix_tc(const PrefixArgs& a, int row_tiles, cudaStream_t st);
 
+std::atomic<int> g_prefix_path{0};  // 0: chosen per call, 1: mma.sync, 2: tcgen05
+
 namespace {
 
 using namespace prefix;
@@ -553,10 +555,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (int64_t)row * kD + 4 * lane) = o;
 }
 
-// Rows of a KV head from which on the prefix goes to the tensor cores of
-// tcgen05. 32768 keys x 8 heads: 16 rows 31 us on mma.sync and 40 on tcgen05,
-// 24 rows 45 (three or four groups of 8) and 40.
-constexpr int64_t kTcRows = 17;
+// Which kernel takes the prefix. On mma.sync the time grows with 16-row groups
+// times keys (45 ps each, the GPU full), on tcgen05 with row tiles times keys
+// (114 ps a key for 128 rows, 145 for 256) from about 10 us more. 8 KV heads,
+// mma.sync against tcgen05: 64 rows 14 and 16 us at 4096 keys, 30 and 27 at
+// 16384; 256 rows 22 and 24 us at 2048, 31 and 26 at 4096, 96 and 41 at 16384;
+// 32 rows 20 and 26 us at 16384, never the other way.
+bool prefix_on_tc(int64_t Hkv, int64_t rows, int64_t P, int tiles, int groups_of_tiles) {
+  const int64_t gain = 45 * ((rows + 15) / 16) - (tiles == 2 ? 145 : 114) * groups_of_tiles;
+  return gain > 0 && Hkv * P > 10000000 / gain;
+}
 
 // How a problem is cut: the same for the workspace query and the launch.
 struct Plan {
@@ -570,25 +578,29 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
   Plan pl;
   const int64_t R = Hq / Hkv, rows = B * R, sms = num_sms();
   const int64_t step = kWarps * kStep;
-  const int64_t want = sms * 4;  // CTAs: four of a wave's fit an SM
-  auto cut = [&](int64_t keys, int64_t others, int& chunk, int& n) {
+  auto cut = [&](int64_t keys, int64_t others, int64_t want, int& chunk, int& n) {
     const int64_t ranges =
         std::max<int64_t>(1, std::min<int64_t>((keys + step - 1) / step, want / others));
     chunk = (int)(((keys + ranges - 1) / ranges + step - 1) / step * step);
     n = (int)((keys + chunk - 1) / chunk);
   };
   pl.nto = R <= 8 ? 1 : 2;
-  pl.ntp = rows <= 8 || P == 0 ? 1 : 2;
+  pl.ntp = 1;
+  int64_t wave = pl.nto == 1 ? 4 * sms : 2 * sms;  // CTAs that fit at once
   pl.tc = 0;
   pl.nsp = pl.ranges = 0;
   pl.nrt = 0;
   pl.chunk_p = 128;
-  if (P > 0 && rows >= kTcRows) {
+  const int64_t rt = (rows + 127) / 128;
+  const int per = rt >= 2 ? 2 : 1;
+  const int64_t rg = (rt + per - 1) / per;
+  const int path = g_prefix_path.load(std::memory_order_relaxed);
+  if (P > 0 && (path == 2 || (path == 0 && prefix_on_tc(Hkv, rows, P, per, (int)rg)))) {
     // tcgen05: the ranges that give the slowest SM the least work, a CTA's
     // start and end counted as 4 tiles
-    const int64_t tiles = (P + 127) / 128, rt = (rows + 127) / 128;
-    pl.tc = rt >= 2 ? 2 : 1;
-    pl.nrt = (int)((rt + pl.tc - 1) / pl.tc);
+    const int64_t tiles = (P + 127) / 128;
+    pl.tc = per;
+    pl.nrt = (int)rg;
     // (about two waves at most; 2^24 units fill any number of SMs with one range)
     const uint32_t units = (uint32_t)std::min<int64_t>(Hkv * pl.nrt, 1 << 24);
     uint64_t best = UINT64_MAX;
@@ -596,21 +608,27 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
         tiles, std::max<uint32_t>(8, 2 * (uint32_t)sms / units + 1));
     for (uint32_t n = 1; n <= most; ++n) {
       const uint32_t waves = (units * n + (uint32_t)sms - 1) / (uint32_t)sms;
-      const uint32_t per = ((uint32_t)tiles + n - 1) / n;
-      const uint64_t cost = (uint64_t)waves * (per + 4);
+      const uint32_t run = ((uint32_t)tiles + n - 1) / n;
+      const uint64_t cost = (uint64_t)waves * (run + 4);
       if (cost < best) {
         best = cost;
-        pl.chunk_p = (int)per * 128;
+        pl.chunk_p = (int)run * 128;
       }
     }
     pl.ranges = (int)((P + pl.chunk_p - 1) / pl.chunk_p);
     pl.nsp = pl.tc == 1 ? 2 * pl.ranges : pl.ranges;
   } else if (P > 0) {
+    // 16 rows share a key's loads, at half the warps; where the sequences' own
+    // tokens are most of the work they run better beside 8 rows (64 sequences
+    // x 8 heads, 512 own tokens, 128 shared: 18.4 us, 21.4 with 16 rows; 128
+    // own, 1024 shared: 23.7 with 16 rows)
+    pl.ntp = rows <= 8 || (R <= 8 && B * cap > (rows + 15) / 16 * P) ? 1 : 2;
+    wave = pl.ntp * pl.nto == 1 ? 4 * sms : 2 * sms;
     pl.nrt = (int)((rows + 8 * pl.ntp - 1) / (8 * pl.ntp));
-    cut(P, std::max<int64_t>(1, Hkv * pl.nrt), pl.chunk_p, pl.ranges);
+    cut(P, std::max<int64_t>(1, Hkv * pl.nrt), wave, pl.chunk_p, pl.ranges);
     pl.nsp = pl.ranges;
   }
-  cut(cap, std::max<int64_t>(1, B * Hkv), pl.chunk_o, pl.nso);
+  cut(cap, std::max<int64_t>(1, B * Hkv), wave, pl.chunk_o, pl.nso);
   return pl;
 }
 
@@ -651,7 +669,7 @@ wq_status launch(const PrefixArgs& a, int tc, cudaStream_t st) {
 template <int NTO>
 wq_status launch_o(const PrefixArgs& a, const Plan& pl, cudaStream_t st) {
   // (R > 8 has more than 8 rows: a prefix on mma.sync then takes two groups)
-  if (NTO == 1 && (pl.tc || pl.ntp == 1)) return launch<1, 1>(a, pl.tc, st);
+  if (NTO == 1 && pl.ntp == 1) return launch<1, 1>(a, pl.tc, st);
   return launch<2, NTO>(a, pl.tc, st);
 }
 

@@ -568,7 +568,7 @@ wq_status wq_workspace_bytes(wq_op op, int64_t M, int64_t N, int64_t K,
  * exists so that the timeout path can be exercised without a device fault.
  * It applies to every later launch, in this process, of the kernels with
  * bounded waits (the tensor-core kernels of wq_w4a16_gemm, of wq_mx_gemm, of
- * wq_prefix_attention for more than 16 query rows a KV head, and of wq_msd_gemm
+ * wq_prefix_attention for large batches on long prefixes, and of wq_msd_gemm
  * for M > 16):
  *   limit_ns  how long any one device wait may last before the kernel gives
  *             up; 0 restores the default of 2 s;
@@ -595,6 +595,17 @@ wq_status wq_test_set_wait(uint64_t limit_ns, int stall);
  * made from another thread. Returns WQ_ERR_INVALID_ARG outside 0..64.
  */
 wq_status wq_test_set_attention_split(int32_t chunks_per_cta);
+
+/*
+ * Test hook for wq_prefix_attention. The pages have no counterpart: it exists
+ * so that tests can reach either kernel for the prefix at any size. By default
+ * (0) the kernel is chosen per call from the sizes; 1 takes the warp-level MMAs
+ * and 2 the tcgen05 tensor cores for every later call, and workspace query, in
+ * this process; results differ by the two kernels' roundings. Host only;
+ * process-wide; change it only while no such call is being made from another
+ * thread. Returns WQ_ERR_INVALID_ARG outside 0..2.
+ */
+wq_status wq_test_set_prefix_path(int32_t path);
 
 /*
  * Read (and, if `clear` != 0, reset) the library's sticky device error word,

@@ -85,6 +85,19 @@ def test_prefix_attention_validation(wq):
         wq.WQ_ERR_INVALID_ARG
 
 
+def test_prefix_path_hook(wq):
+    assert wq.lib.wq_test_set_prefix_path(3) == wq.WQ_ERR_INVALID_ARG
+    assert wq.lib.wq_test_set_prefix_path(-1) == wq.WQ_ERR_INVALID_ARG
+    sizes = []
+    for path in (1, 2, 0):
+        wq.wq_test_set_prefix_path(path)
+        size = ctypes.c_size_t()
+        assert wq.lib.wq_prefix_attention_workspace(64, 64, 8, 128, 32768, 1024,
+                                                    ctypes.byref(size)) == wq.WQ_OK
+        sizes.append(size.value)
+    assert sizes[2] in sizes[:2] and min(sizes) > 0
+
+
 def _planes(wq, x=A16, dt=0, ldx=512, m=4, k=512, n=2, c=A16, s=A16):
     return wq.lib.wq_mx_quantize_planes(x, dt, ldx, m, k, n, c, s, None)
 

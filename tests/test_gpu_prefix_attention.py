@@ -35,6 +35,14 @@ def wq():
     return binding
 
 
+@pytest.fixture(autouse=True, params=[0, 1, 2], ids=["auto", "mma", "tcgen05"])
+def path(wq, request):
+    """Every test on the chosen kernel and on both."""
+    wq.wq_test_set_prefix_path(request.param)
+    yield request.param
+    wq.wq_test_set_prefix_path(0)
+
+
 def _cache(wq, b, h, cap, seed, k_scale=0.5, v_scale=1.0):
     """(device K, device V, host K, host V) of quantized Gaussian rows."""
     g = torch.Generator().manual_seed(seed)
@@ -323,6 +331,7 @@ def test_refusals(wq):
 def test_bounded_wait_expires_cleanly(wq, b):
     """With the first key tile withheld the tensor-core kernel gives up, reports
     the wait and returns; the next call is right."""
+    wq.wq_test_set_prefix_path(2)
     hq, hkv, cap, p = 8, 1, 16, 700
     pk, pv, hpk, hpv = _cache(wq, 1, hkv, p, 30)
     k, v, hk, hv = _cache(wq, b, hkv, cap, 31)
