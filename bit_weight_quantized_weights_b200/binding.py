@@ -628,6 +628,8 @@ def _kv_rows(k, v, cache, starts, offsets, dev):
             not starts.is_contiguous() or not offsets.is_contiguous():
         raise ValueError("starts must be int32 [%d] and offsets int32 [%d], contiguous" % (b, b + 1))
     _on_device(dev, k, v, starts, offsets)
+    if shape[0] == 1 or hkv == 1:  # the stride of one element means nothing
+        ks, vs = ((s[0] if shape[0] > 1 else 0, s[1] if hkv > 1 else 0) for s in (ks, vs))
     return shape[0], dt, _Strides(ks[0], ks[1]), _Strides(vs[0], vs[1])
 
 

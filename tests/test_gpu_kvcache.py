@@ -124,6 +124,25 @@ def test_strided_rows(wq, dtype):
     assert bool((big[0] == 7).all()) and bool((big[-1] == 7).all())
 
 
+def test_one_token_or_head_of_any_stride(wq):
+    """The stride of a dimension of one element means nothing."""
+    h, cap = 2, 9
+    g = torch.Generator().manual_seed(77)
+    for shape in ((1, h), (3, 1)):
+        x = torch.randn(shape[0], 2 * shape[1] * D + (4 if shape[0] == 1 else 0), generator=g)
+        x = x.bfloat16().cuda()
+        n = shape[1] * D
+        k, v = (x[:, i * n:(i + 1) * n].unflatten(1, (shape[1], D)) for i in (0, 1))
+        if shape[1] == 1:
+            k, v = (t.as_strided(t.shape, (t.stride(0), 4, 1), t.storage_offset()) for t in (k, v))
+        starts, offsets = _i32([1]), _i32([0, shape[0]])
+        caches = [wq.kv_cache_alloc(1, shape[1], cap) for _ in range(2)]
+        wq.wq_kv_append(k, v, *caches[0], starts, offsets)
+        wq.wq_kv_append(k.contiguous(), v.contiguous(), *caches[1], starts, offsets)
+        for a, b in zip(caches[0][0] + caches[0][1], caches[1][0] + caches[1][1]):
+            assert torch.equal(a, b)
+
+
 def test_values_on_rounding_borders(wq):
     """Rows of zeros, of one sign, of a single large value, subnormal ranges,
     halfway codes, and the largest finite bf16 that fits fp16 scales."""
