@@ -69,8 +69,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float pow2(int x) { return __uint_as_float((uint32_t)(127 + x) << 23); }
 
 // The scale's leading 7 bits, whose product with q - z (4 bits) is exact in
-// fp16, and what is left of it: s / head - 1 < 2^-6 (2^-15 as bf16).
-__device__ __forceinline__ uint32_t scale_head(uint32_t bits) { return bits & 0xFFF0u; }
+// fp16, and what is left of it: s / head - 1 < 2^-6 (2^-15 as bf16). Subnormal
+// scales have 10 bits at most and no leading one of their own: from 2^7 units on
+// the lowest 3 go (s / head - 1 < 2^-4, 2^-13 as bf16), below that none.
+__device__ __forceinline__ uint32_t scale_head(uint32_t bits) {
+  return bits & (bits >= 0x400u ? 0xFFF0u : bits >= 0x80u ? 0xFFF8u : 0xFFFFu);
+}
 __device__ __forceinline__ float scale_rest(uint32_t bits) {
   const float h = __half2float(__ushort_as_half((unsigned short)scale_head(bits)));
   const float s = __half2float(__ushort_as_half((unsigned short)bits));

@@ -68,7 +68,7 @@ def _i32(v):
     return torch.tensor(list(v), dtype=torch.int32, device="cuda")
 
 
-def _check(out, q, pk, pv, k, v, lengths, prefix_len):
+def _check(out, q, pk, pv, k, v, lengths, prefix_len, smallest=0.0):
     qn = q.double().cpu().numpy()
     want = kvcache.prefix_attention(qn, pk, pv, k, v, lengths, prefix_len)
     b_, hq, d = qn.shape
@@ -97,7 +97,7 @@ def _check(out, q, pk, pv, k, v, lengths, prefix_len):
                 + (p * delta) @ vv + o * (p * delta).sum(axis=1, keepdims=True))
     half = torch.finfo(out.dtype).eps / 2
     got = out.double().cpu().numpy()
-    bound = slack + half * (np.abs(want) + slack) + 1e-30
+    bound = slack + half * (np.abs(want) + slack) + 1e-30 + smallest
     bad = ~(np.abs(got - want) <= bound)
     assert not bad.any(), "%d elements off, worst %.2f of the bound" % (
         bad.sum(), float((np.abs(got - want) / bound).max()))
@@ -106,7 +106,8 @@ def _check(out, q, pk, pv, k, v, lengths, prefix_len):
     # step / sqrt(3)); twice the half step leaves room for peaked rows.
     norm = np.linalg.norm(want)
     if out.numel() > 1000 and norm > 0:
-        assert np.linalg.norm(got - want) <= 2 * half * norm + 2.0 ** -10 * norm
+        assert np.linalg.norm(got - want) <= (2 * half + 2.0 ** -10) * norm \
+            + smallest * np.sqrt(want.size)
 
 
 def _rows_of(cache, b, h, n):
@@ -204,6 +205,26 @@ def test_extreme_magnitudes(wq, b):
     lengths[0] = 0                                       # only the tiny values of the prefix
     out = wq.wq_prefix_attention(q, pk, pv, k, v, _i32(lengths))
     _check(out, q, hpk, hpv, hk, hv, lengths, p)
+
+
+@pytest.mark.parametrize("which", ["keys", "values"])
+@pytest.mark.parametrize("scale", [5e-7, 2e-6, 1.5e-5, 1e-4])
+def test_rows_whose_scales_are_subnormal(wq, scale, which):
+    """fp16 scales of 3 to 650 times 2^-24: few keys, so that a row whose value
+    is lost shows. Beyond the bound above, an fp16 output below 2^-14 is off by
+    half of fp16's smallest number, 2^-25."""
+    b, hq, p = 9, 16, 5
+    g = torch.Generator().manual_seed(31)
+    pk, pv, hpk, hpv = _cache(wq, 1, 1, p, 32, k_scale=scale if which == "keys" else 0.5,
+                              v_scale=scale if which == "values" else 1.0)
+    k, v, hk, hv = _cache(wq, b, 1, 8, 33)
+    q = torch.randn(b, hq, D, generator=g)
+    if which == "keys":
+        q = (q * 2e4).clamp(-6e4, 6e4)
+    q = q.half().cuda()
+    lengths = [0] * b
+    out = wq.wq_prefix_attention(q, pk, pv, k, v, _i32(lengths))
+    _check(out, q, hpk, hpv, hk, hv, lengths, p, smallest=2.0 ** -25)
 
 
 @pytest.mark.parametrize("b", [2, 40])
