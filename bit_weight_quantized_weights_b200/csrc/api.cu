@@ -180,7 +180,7 @@ wq_status check_prefix_shape(int64_t B, int64_t Hq, int64_t Hkv, int32_t D, int6
   if (B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || P < 0 || cap <= 0 || Hq % Hkv != 0)
     return WQ_ERR_INVALID_ARG;
   if (D != 128 || Hq / Hkv > 16) return WQ_ERR_UNSUPPORTED;
-  if (P > INT32_MAX - 7 || cap > INT32_MAX - 7) return WQ_ERR_UNSUPPORTED;
+  if (P > (1 << 30) || cap > (1 << 30)) return WQ_ERR_UNSUPPORTED;  // key numbers plus a few tiles
   if (B > (1 << 30) || Hq > (1 << 30) || B * Hq > (1 << 30)) return WQ_ERR_UNSUPPORTED;
   return WQ_OK;
 }
@@ -567,7 +567,7 @@ wq_status wq_prefix_attention(const void* q, wq_dtype dtype, int64_t q_stride, i
   if (s != WQ_OK) return s;
   if ((dtype != WQ_BF16 && dtype != WQ_FP16) || q_stride < 0 || P > prefix_cap)
     return WQ_ERR_INVALID_ARG;
-  if (prefix_cap > INT32_MAX - 7) return WQ_ERR_UNSUPPORTED;
+  if (prefix_cap > (1 << 30)) return WQ_ERR_UNSUPPORTED;
   if (B == 0) return WQ_OK;
   const void* const pre[6] = {prefix_k_codes, prefix_k_scales, prefix_k_zeros,
                               prefix_v_codes, prefix_v_scales, prefix_v_zeros};

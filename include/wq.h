@@ -390,8 +390,9 @@ wq_status wq_mx_gemv(const void* x, int64_t M, int64_t N, int64_t K, int32_t n_p
  *   in the tensor core and accumulate in fp32; one rounding to bf16. M == 0 or
  *   N == 0: no-op. Requires K % 128 == 0 and N % 16 == 0. Scale bytes of 255
  *   are NaN. Workspace: at least wq_workspace_bytes(WQ_OP_MX_GEMM, M, N, K, 0,
- *   n_planes) bytes; contents on entry do not matter. May return WQ_ERR_TIMEOUT through wq_device_error if an internal
- *   bounded wait expires.
+ *   n_planes) bytes; contents on entry do not matter, and calls that may
+ *   overlap on the GPU need one each. May return WQ_ERR_TIMEOUT through
+ *   wq_device_error if an internal bounded wait expires.
  * Both are asynchronous on `stream`; every buffer is caller-owned.
  */
 wq_status wq_mx_quantize_planes(const void* x, wq_dtype dtype, int64_t ldx, int64_t M, int64_t K,
@@ -481,8 +482,8 @@ wq_status wq_kv_block_values(const uint32_t* codes, int64_t rows, int64_t L, int
  * wq_kv_read writes RN_dtype((q - z) s) of every row (the product is exact in
  * fp32), and rows of zeros for positions outside the cache.
  * `starts` and `offsets` need 4-byte alignment, everything else 16. T == 0 and
- * B == 0 are no-ops. D != 128, T > 2^31 - 1, cap > 2^31 - 8, B > 65535 or
- * (T / 8 + 2 B) * Hkv > 2^31 - 9 return WQ_ERR_UNSUPPORTED. Non-finite rows
+ * B == 0 are no-ops. D != 128, T > 2^31 - 1, cap > 2^31 - 8, B or Hkv > 65535
+ * or (T / 8 + 2 B) * Hkv > 2^31 - 9 return WQ_ERR_UNSUPPORTED. Non-finite rows
  * give unspecified codes. Rows that repeat a cache position through
  * overlapping sequences do not exist (every sequence has its own cache rows);
  * offsets that decrease give unspecified rows, inside the buffers.
@@ -519,11 +520,14 @@ wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_ze
  *            length 0) gets zeros.
  * Tokens behind P and behind a sequence's length are not read, whatever the
  * buffers hold there. The codes enter fp16 tensor-core products as exact
- * integers and scores, softmax statistics and sums are fp32; the softmax
- * weights are rounded to fp16. Scales are those a quantizer writes (positive
- * and finite). The result of a sequence does not depend on the values of
- * other sequences. B == 0 is a no-op. With P == 0 the six prefix pointers may
- * be NULL. prefix_cap or cap > 2^31 - 8, R > 16, B * Hq or B * R > 2^30 return
+ * integers, except those of the prefix for bf16 queries where the batch is
+ * large: there the dequantized values (q - z) s are rounded to fp16. Scores,
+ * softmax statistics and sums are fp32; the softmax weights are rounded to
+ * fp16. Scales are those a quantizer writes (positive and finite); scores are
+ * below 2^99 in magnitude. The result of a sequence does not depend on the
+ * values of other sequences (a query that is not finite spoils its own row
+ * only). B == 0 is a no-op. With P == 0 the six prefix pointers may be NULL.
+ * prefix_cap or cap > 2^30, R > 16 or B * Hq > 2^30 return
  * WQ_ERR_UNSUPPORTED. Workspace: at least wq_prefix_attention_workspace(...)
  * bytes for the same sizes; contents on entry do not matter, and calls that
  * may overlap on the GPU need one each. May return WQ_ERR_TIMEOUT through

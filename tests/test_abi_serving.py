@@ -66,7 +66,8 @@ def test_prefix_attention_validation(wq):
                 dict(out=None), dict(pre=(None,) * 6), dict(own=(A16,) * 5 + (None,))):
         assert _attn(wq, **bad) == wq.WQ_ERR_INVALID_ARG, bad
     for bad in (dict(d=64), dict(hq=34), dict(cap=2 ** 31 - 1), dict(p=2 ** 31 - 1, pcap=2 ** 31),
-                dict(pcap=2 ** 31 - 1), dict(b=2 ** 28)):
+                dict(pcap=2 ** 31 - 1), dict(cap=2 ** 30 + 1), dict(pcap=2 ** 30 + 1),
+                dict(b=2 ** 28)):
         assert _attn(wq, **bad) == wq.WQ_ERR_UNSUPPORTED, bad
     for bad in (dict(q=MIS), dict(out=MIS), dict(ln=A16 + 2), dict(stride=1028), dict(ws=MIS),
                 dict(pre=(A16, MIS) + (A16,) * 4), dict(own=(MIS,) + (A16,) * 5)):
