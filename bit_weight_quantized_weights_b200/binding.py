@@ -463,12 +463,12 @@ def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     if xs[1] != 1 and k > 1:
         raise ValueError("the rows of x must be contiguous")
     if planes is None:
-        planes = torch.empty((n_planes, m, k // 2), dtype=torch.uint8, device=x.device)
+        planes = x.new_empty((n_planes, m, k // 2), dtype=torch.uint8)
     elif planes.dtype is not torch.uint8 or planes.shape != (n_planes, m, k // 2) or \
             not planes.is_contiguous():
         raise ValueError("planes must be uint8 [%d, %d, %d]" % (n_planes, m, k // 2))
     if scales is None:
-        scales = torch.empty((n_planes, m, k // 32), dtype=torch.uint8, device=x.device)
+        scales = planes.new_empty((n_planes, m, k // 32))
     elif scales.dtype is not torch.uint8 or scales.shape != (n_planes, m, k // 32) or \
             not scales.is_contiguous():
         raise ValueError("scales must be uint8 [%d, %d, %d]" % (n_planes, m, k // 32))
@@ -504,7 +504,7 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
     if workspace is None:
         workspace = mx_gemm_workspace(m, n, k, p, planes.device)
     if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=planes.device)
+        out = planes.new_empty((m, n), dtype=torch.bfloat16)
     elif out.dtype is not torch.bfloat16 or out.shape != (m, n) or not out.is_contiguous():
         raise ValueError("y must be bfloat16 [%d, %d], contiguous" % (m, n))
     _on_device(dev, planes, plane_scales, codes, scales, workspace, out)
@@ -658,9 +658,10 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
     dev = _current_device()
     b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     if k_out is None:
-        k_out = torch.empty((total, hkv, d), dtype=dtype, device=k_cache[0].device)
+        k_out = k_cache[1].new_empty((total, hkv, d), dtype=dtype)
     if v_out is None:
-        v_out = torch.empty((total, hkv, d), dtype=dtype, device=k_cache[0].device)
+        v_out = torch.empty_like(k_out) if k_out.is_contiguous() else \
+            k_out.new_empty((total, hkv, d))
     t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets, dev)
     if t != total:
         raise ValueError("k_out and v_out must have %d rows" % total)
@@ -714,7 +715,7 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
     if workspace is None:
         workspace = prefix_attention_workspace(b, hq, hkv, prefix_len, cap, d, q.device)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
     elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must have q's type and shape, contiguous")
     _on_device(dev, q, lengths, workspace, out)
