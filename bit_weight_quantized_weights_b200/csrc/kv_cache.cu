@@ -217,6 +217,19 @@ __device__ __forceinline__ int code_of(float v, int z) {
   return __viaddmin_s32_relu(__float_as_int(__fadd_rn(v, 12582912.0f)), z - 0x4B400000, 15);
 }
 
+// The code of element a of a row with scale s, y = RN(1 / s). A quotient of a
+// 16-bit element (11 bits) and s (11 bits) is a half-integer or at least 2^-13
+// away from every one, and a y is off by at most 30 * 2^-24: rounded to 2^-16
+// (the spacing around 192) it is a tie where a / s is one and on the same side
+// of it elsewhere. Two operations instead of the four of the quotient itself.
+template <typename T>
+__device__ __forceinline__ int code_of(float a, float s, float y, int z) {
+  if (sizeof(T) == 4) return code_of(div_by(a, s, y), z);
+  return __viaddmin_s32_relu(
+      __float_as_int(__fadd_rn(__fmaf_rn(a, y, 192.0f), 12582912.0f - 192.0f)), z - 0x4B400000,
+      15);
+}
+
 // Scale, its reciprocal and the zero of a row's range.
 __device__ __forceinline__ void row_scale(float lo, float hi, __half& sh, float& s, float& y,
                                           int& z) {
@@ -298,17 +311,17 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 4)
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      word |= (uint32_t)code_of(div_by(f[i], sr, yr), zr) << (4 * i);
+      word |= (uint32_t)code_of<T>(f[i], sr, yr, zr) << (4 * i);
     if (w.tok[r] >= 0) kc[(row0 + 2 * r + half) * (kD / 8) + col] = word;
     from += 4;
     sr = __shfl_sync(0xffffffffu, s, from);
     yr = __shfl_sync(0xffffffffu, y, from);
     zr = __shfl_sync(0xffffffffu, z, from);
     vr[r].get(f);
-    const int bit = 4 * (2 * r + half);
+    const uint32_t place = half ? 16u << (8 * r) : 1u << (8 * r);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      words[i] |= (uint32_t)code_of(div_by(f[i], sr, yr), zr) << bit;
+      words[i] += (uint32_t)code_of<T>(f[i], sr, yr, zr) * place;
   }
   {
     const int r = col & 3;
