@@ -59,10 +59,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // ..): row r is kept at place r ^ (r / 4 % 2), piece q of block t4 at q ^ 2 t4,
 // so that the 8 lanes of a phase read distinct banks. The step's scales and
 // zeros, which may lie at any 2-byte address, are loaded a step ahead in
-// registers (a token a lane) and put beside.
+// registers (a token a lane) and put beside, V's scale as its logarithm and its
+// inverse: worked out once a token instead of by the 4 lanes that use it.
 constexpr int kStages = 3;
 constexpr int kStageBytes = kStep * kD;                    // codes of 32 keys, K and V
-constexpr int kScaleBytes = 4 * kStep * 2;                 // sk, zk, sv, zv
+constexpr int kScaleBytes = kStep * 16;  // sk, log2(sv), 1 / sv in fp32, zk, zv in fp16
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 
 template <int NT>
@@ -79,26 +80,35 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
                : "memory");
 }
 
-// Codes of the step at token l0 into a stage (tokens from `end` on: zeros).
-__device__ __forceinline__ void load_codes(uint32_t stage, const Cache& c, int64_t crow0,
-                                           int64_t vrow0, int l0, int end, int lane) {
+// Codes of the step at token l0 < end into a stage (tokens from `end` on: zeros).
+// kp and vp are this lane's pieces of the step's first rows and of its first block.
+__device__ __forceinline__ void load_codes(uint32_t stage, const uint32_t* kp, const uint32_t* vp,
+                                           int l0, int end, int lane) {
+  const int r = lane >> 2;
+  const uint32_t kd = stage + (uint32_t)((r ^ (r >> 2)) * 64 + 16 * (lane & 3));
+  const uint32_t vd = stage + kStep * 64;
+  if (l0 + kStep <= end) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    const bool in = l0 + r < end;
-    cp_async16(stage + (uint32_t)((r ^ ((r >> 2) & 1)) * 64 + 16 * (lane & 3)),
-               c.kc + (crow0 + (in ? l0 + r : 0)) * (kD / 8) + 4 * (lane & 3), in);
-  }
+    for (int i = 0; i < 4; ++i) cp_async16(kd + 512 * i, kp + 8 * i * (kD / 8), true);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int blk = (l0 >> 3) + i;
-    const bool in = 8 * blk < end;
-    cp_async16(stage + (uint32_t)(kStep * 64 + i * 512 + ((lane ^ (2 * i)) << 4)),
-               c.vc + (vrow0 + (in ? blk : 0)) * kD + 4 * lane, in);
+    for (int i = 0; i < 4; ++i)
+      cp_async16(vd + i * 512 + ((lane ^ (2 * i)) << 4), vp + i * kD, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = l0 + 8 * i + r < end;
+      cp_async16(kd + 512 * i, in ? kp + 8 * i * (kD / 8) : kp - r * (kD / 8), in);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = l0 + 8 * i < end;
+      cp_async16(vd + i * 512 + ((lane ^ (2 * i)) << 4), in ? vp + i * kD : vp, in);
+    }
   }
 }
 
-// The lane's token of the step at l0: sk, zk, sv, zv as bits (from `end` on: 1 and 0).
+// The lane's token of the step at l0: sk, zk, sv, zv as bits (from `end` on: 1 and 0);
+// and the same put into shared memory.
 __device__ __forceinline__ void load_scales(uint16_t (&s)[4], const Cache& c, int64_t crow0, int l0,
                                             int end, int lane) {
   const bool in = l0 + lane < end;
@@ -107,6 +117,18 @@ __device__ __forceinline__ void load_scales(uint16_t (&s)[4], const Cache& c, in
   s[1] = in ? reinterpret_cast<const uint16_t*>(c.kz)[at] : (uint16_t)0;
   s[2] = in ? reinterpret_cast<const uint16_t*>(c.vs)[at] : (uint16_t)0x3C00u;
   s[3] = in ? reinterpret_cast<const uint16_t*>(c.vz)[at] : (uint16_t)0;
+}
+
+__device__ __forceinline__ void store_scales(uint8_t* dst, const uint16_t (&s)[4], int lane) {
+  auto value = [](uint16_t b) { return __half2float(__ushort_as_half(b)); };
+  float* f = reinterpret_cast<float*>(dst) + lane;
+  const float l = __log2f(fmaxf(value(s[2]), 5.9604645e-8f));  // fp16's smallest: 0 has no log
+  f[0] = value(s[0]);
+  f[kStep] = l;
+  f[2 * kStep] = ex2(-l);
+  uint16_t* z = reinterpret_cast<uint16_t*>(dst + 12 * kStep) + lane;
+  z[0] = s[1];
+  z[kStep] = s[3];
 }
 
 // The query rows row0 + n (n < nrows, at most 8 NT) of KV head kh against keys
@@ -119,23 +141,29 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
   const int g = lane >> 2, t4 = lane & 3;
   const uint32_t ring = smem_u32(sm) + (uint32_t)(warp * kStages * kStageBytes);
   const uint8_t* ring_p = sm + warp * kStages * kStageBytes;
-  uint16_t* scl = reinterpret_cast<uint16_t*>(sm + kRingBytes + warp * 2 * kScaleBytes);
+  uint8_t* scl = sm + kRingBytes + warp * 2 * kScaleBytes;
   uint2* qsm = reinterpret_cast<uint2*>(sm + kRingBytes + kWarps * 2 * kScaleBytes);
   float* msm = reinterpret_cast<float*>(sm + kRingBytes + kWarps * 2 * kScaleBytes +
                                         (NT > 1 ? NT * 2048 : 0));  // [warps][8 NT] m, then E
   constexpr int kStride = kWarps * kStep;
   int l0 = begin + warp * kStep;
   uint16_t sc4[4];
+  // (a piece of the next step to load: in the cache, or where no step is left not used)
+  const uint32_t* kp = c.kc + (crow0 + l0 + (lane >> 2)) * (kD / 8) + 4 * (lane & 3);
+  const uint32_t* vp = c.vc + (vrow0 + (l0 >> 3)) * kD + 4 * lane;
+  auto next_codes = [&](int stage, int at) {
+    load_codes(ring + (uint32_t)stage * kStageBytes, kp, vp, at, end, lane);
+    kp += kStride * (kD / 8);
+    vp += kStride / 8 * kD;
+  };
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    if (l0 + s * kStride < end)
-      load_codes(ring + s * kStageBytes, c, crow0, vrow0, l0 + s * kStride, end, lane);
+    if (l0 + s * kStride < end) next_codes(s, l0 + s * kStride);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   if (l0 < end) {
     load_scales(sc4, c, crow0, l0, end, lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) scl[i * kStep + lane] = sc4[i];
+    store_scales(scl, sc4, lane);
     if (l0 + kStride < end) load_scales(sc4, c, crow0, l0 + kStride, end, lane);
   }
 
@@ -222,20 +250,16 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();  // the step is complete, and the stage of the step before is read
     if (l0 + (kStages - 1) * kStride < end)
-      load_codes(ring + (uint32_t)((k + kStages - 1) % kStages) * kStageBytes, c, crow0, vrow0,
-                 l0 + (kStages - 1) * kStride, end, lane);
+      next_codes((k + kStages - 1) % kStages, l0 + (kStages - 1) * kStride);
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (l0 + kStride < end) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) scl[((k + 1) & 1) * (4 * kStep) + i * kStep + lane] = sc4[i];
+      store_scales(scl + ((k + 1) & 1) * kScaleBytes, sc4, lane);
       if (l0 + 2 * kStride < end) load_scales(sc4, c, crow0, l0 + 2 * kStride, end, lane);
     }
     const uint8_t* stage = ring_p + (k % kStages) * kStageBytes;
-    const uint16_t* sp = scl + (k & 1) * (4 * kStep);
-    const uint2 ssk = *reinterpret_cast<const uint2*>(sp + 4 * g);
-    const uint2 szk = *reinterpret_cast<const uint2*>(sp + kStep + 4 * g);
-    const uint2 ssv = *reinterpret_cast<const uint2*>(sp + 2 * kStep + 4 * g);
-    const uint4 szv = *reinterpret_cast<const uint4*>(sp + 3 * kStep + 8 * t4);
+    const uint8_t* sp = scl + (k & 1) * kScaleBytes;
+    const uint2 szk = *reinterpret_cast<const uint2*>(sp + 12 * kStep + 8 * g);
+    const uint4 szv = *reinterpret_cast<const uint4*>(sp + 14 * kStep + 16 * t4);
     // ---- scores: S^T tile s holds tokens 4 g + 2 s (rows g) and + 1 (rows
     // g + 8) against the query rows 2 t4, 2 t4 + 1
     float sc[NT][2][4];
@@ -247,19 +271,11 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
       z1[i] = h2(__hadd2(as_h2(zk2[i]), as_h2(0x64006400u)));
       z64[i] = h2(__hneg2(__hadd2(as_h2(zk2[i]), as_h2(0x54005400u))));
     }
-    float skf[4], lsv[4], rsv[4];
-    {
-      const float2 s01 = __half22float2(as_h2(ssk.x)), s23 = __half22float2(as_h2(ssk.y));
-      const float2 v01 = __half22float2(as_h2(ssv.x)), v23 = __half22float2(as_h2(ssv.y));
-      skf[0] = s01.x, skf[1] = s01.y, skf[2] = s23.x, skf[3] = s23.y;
-      const float v[4] = {v01.x, v01.y, v23.x, v23.y};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = fmaxf(v[i], 5.9604645e-8f);  // fp16's smallest: a scale of 0 has no log
-        lsv[i] = __log2f(x);
-        rsv[i] = ex2(-lsv[i]);
-      }
-    }
+    const float4 skf = *reinterpret_cast<const float4*>(sp + 16 * g);
+    const float4 lsv = *reinterpret_cast<const float4*>(sp + 4 * kStep + 16 * g);
+    const float4 rsv = *reinterpret_cast<const float4*>(sp + 8 * kStep + 16 * g);
+    const float sk4[4] = {skf.x, skf.y, skf.z, skf.w}, lv4[4] = {lsv.x, lsv.y, lsv.z, lsv.w},
+                rv4[4] = {rsv.x, rsv.y, rsv.z, rsv.w};
     uint32_t y1[2], y64[2];  // k-step s: zeros of tokens (2s, 2s + 4), and (2s + 1, 2s + 5)
     y1[0] = h2(__hadd2(as_h2(prmt(szv.x, szv.z, 0x5410)), as_h2(0x64006400u)));
     y1[1] = h2(__hadd2(as_h2(prmt(szv.y, szv.w, 0x5410)), as_h2(0x64006400u)));
@@ -297,7 +313,6 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
         }
     }
     // ---- weights
-    const int left = end - (l0 + 4 * g);  // this lane's tokens i < left exist
     bool grow = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -306,10 +321,26 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 2 * s + (r >> 1);  // token 4 g + i
-          const float t = fmaf(sc[nt][s][r] * cr[nt][r & 1], skf[i], lsv[i]);
-          sc[nt][s][r] = i < left ? t : -INFINITY;
-          grow |= sc[nt][s][r] > m[nt][r & 1] + kSlack;
+          sc[nt][s][r] = fmaf(sc[nt][s][r] * cr[nt][r & 1], sk4[i], lv4[i]);
         }
+    if (l0 + kStep > end) {
+      const int left = end - (l0 + 4 * g);  // this lane's tokens i < left exist
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (2 * s + (r >> 1) >= left) sc[nt][s][r] = -INFINITY;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float top = fmaxf(fmaxf(sc[nt][0][x], sc[nt][0][2 + x]),
+                                fmaxf(sc[nt][1][x], sc[nt][1][2 + x]));
+        grow |= top > m[nt][x] + kSlack;
+      }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -340,7 +371,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           w[r] = ex2(sc[nt][s][r] - m[nt][r & 1]);
-          E[nt][r & 1] = fmaf(w[r], rsv[2 * s + (r >> 1)], E[nt][r & 1]);
+          E[nt][r & 1] = fmaf(w[r], rv4[2 * s + (r >> 1)], E[nt][r & 1]);
         }
         bp[nt][s][0] = transpose8x8(pack_f16x2(w[0], w[1]));
         bp[nt][s][1] = transpose8x8(pack_f16x2(w[2], w[3]));
