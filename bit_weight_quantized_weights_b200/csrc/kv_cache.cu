@@ -195,9 +195,9 @@ __device__ __forceinline__ uint32_t packed_range(const Row<T>& r) {
   auto bits = [](P v) { return *reinterpret_cast<uint32_t*>(&v); };
   constexpr uint32_t kNeg = 0x80008000u;
   const P n = min2(min2(as(w[0]), as(w[1])), min2(as(w[2]), as(w[3])));
-  const P x = min2(min2(as(w[0] ^ kNeg), as(w[1] ^ kNeg)),
-                   min2(as(w[2] ^ kNeg), as(w[3] ^ kNeg)));
-  P m = min2(as(prmt(bits(n), bits(x), 0x5410)), as(prmt(bits(n), bits(x), 0x7632)));
+  const P x = __hmax2(__hmax2(as(w[0]), as(w[1])), __hmax2(as(w[2]), as(w[3])));
+  const uint32_t y = bits(x) ^ kNeg;
+  P m = min2(as(prmt(bits(n), y, 0x5410)), as(prmt(bits(n), y, 0x7632)));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1)
     m = min2(m, as(__shfl_xor_sync(0xffffffffu, bits(m), o)));
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 16)
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      word |= (uint32_t)code_of<T>(f[i], sr, yr, zr) << (4 * i);
+      word += (uint32_t)code_of<T>(f[i], sr, yr, zr) << (4 * i);
     if (w.tok[r] >= 0) kc[(row0 + 2 * r + half) * (kD / 8) + col] = word;
     from += 4;
     sr = __shfl_sync(0xffffffffu, s, from);
