@@ -8,9 +8,11 @@
 // tokens (uint32 [B, Hkv, ceil(cap / 8), 128]: token t of dimension d in
 // nibble t % 8). A row read back is RN((q - z) s); (q - z) s is exact in fp32.
 //
-// Both kernels stream rows once and are bound by HBM: per row of 128 elements
-// the append reads 256 B (16-bit types) and writes 68 B, the read-back the
-// reverse. The unit of work is one V block, 8 cache positions of one
+// Both kernels stream rows once: per row of 128 elements the append reads 256 B
+// (16-bit types) and writes 68 B, the read-back the reverse. The read is bound by
+// HBM (127315 tokens x 8 heads, bf16: 660 MB in 110 us, 91% of a copy's rate), the
+// append by its instructions, about 1000 a warp for 16 rows (12891 tokens x 8
+// heads: 67 MB in 17.3 us, 59% of a copy's rate). The unit of work is one V block, 8 cache positions of one
 // (sequence, head), taken by one warp: 16 lanes hold a row (8 elements a lane,
 // one 16-byte access), the two halves of the warp hold two rows, four steps
 // cover the block. So a V word has one writer (no atomics; the nibbles of
@@ -33,10 +35,11 @@ namespace {
 
 constexpr int kD = 128;
 // Warps of a CTA and CTAs an SM: the warps share nothing, and with small CTAs an
-// SM takes new work the sooner. 127315 tokens x 8 heads read: 124 us with 8 x 4,
-// 120 with 4 x 8, 119 with 2 x 16, 114 with 2 x 18 (56 registers a thread), 116
-// with 2 x 20; the append needs 64 registers (17.9 us for 12891 tokens with
-// 2 x 16, 18.9 with 2 x 18).
+// SM takes new work the sooner (127315 tokens x 8 heads read: 124 us with 8 x 4,
+// 114 with 2 x 18). The read runs 2 x 20 (48 registers a thread): 110 us, 118
+// with 2 x 18, 111 with 4 x 10; 12891 tokens 13.0 us, 12.8 with 2 x 18, 14.0 with
+// 2 x 24. The append needs 64 registers (17.9 us for 12891 tokens with 2 x 16,
+// 18.9 with 2 x 18).
 constexpr unsigned kWarps = 2;
 
 struct KvRows {            // packed rows and where they belong
@@ -361,14 +364,20 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 16)
   *vword = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// (q - z) s of 8 codes given in nibble `sh / 4` of 8 words, or in the 8
-// nibbles of one word: q as a float by placing it in the mantissa of 2^23.
-__device__ __forceinline__ float code_value(uint32_t w, int sh, float zb, float s) {
-  return (__uint_as_float(lop3_and_or(w >> sh, 15u, 0x4B000000u)) - zb) * s;
-}
+// (q - z) s by one fused multiply-add: a code at mantissa bits 12 - 15 (or 16 - 19)
+// of 1.0 is 1 + q / u with u = 2^11 (2^7), and (1 + q / u) (u s) - (u + z) s is
+// exact: u + z has 12 bits at most, s has 11.
+constexpr uint32_t kOne = 0x3F800000u;
+struct Affine {
+  float a, b;
+  __device__ __forceinline__ Affine(float u, float s, float z) : a(u * s), b(-(u + z) * s) {}
+  __device__ __forceinline__ float operator()(uint32_t word, uint32_t mask) const {
+    return __fmaf_rn(__uint_as_float(lop3_and_or(word, mask, kOne)), a, b);
+  }
+};
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 18)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 20)
     kv_read_kernel(KvRows p, const uint32_t* __restrict__ kc, const __half* __restrict__ ks,
                    const __half* __restrict__ kz, const uint32_t* __restrict__ vc,
                    const __half* __restrict__ vs, const __half* __restrict__ vz,
@@ -393,9 +402,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 18)
     const int64_t at = row0 + 2 * r + half;
     kw[r] = ok ? kc[at * (kD / 8) + col] : 0u;
     sk[r] = ok ? __half2float(ks[at]) : 0.0f;
-    zk[r] = ok ? __half2float(kz[at]) + 8388608.0f : 8388608.0f;
+    zk[r] = ok ? __half2float(kz[at]) : 0.0f;
     sv[r] = ok ? __half2float(vs[at]) : 0.0f;
-    zv[r] = ok ? __half2float(vz[at]) + 8388608.0f : 8388608.0f;
+    zv[r] = ok ? __half2float(vz[at]) : 0.0f;
   }
   // all 8 words of this lane's columns: 4 of its own, 4 of the other half's
   const uint32_t own4[4] = {mine.x, mine.y, mine.z, mine.w};
@@ -406,16 +415,26 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 18)
     words[j] = half ? got : own4[j];
     words[4 + j] = half ? own4[j] : got;
   }
+  const uint32_t vmask = half ? 0xF0000u : 0xF000u;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (w.tok[r] < 0) continue;
     float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = code_value(kw[r], 4 * i, zk[r], sk[r]);
+    {
+      const uint32_t w = kw[r];
+      const Affine lo(2048.0f, sk[r], zk[r]), hi(128.0f, sk[r], zk[r]);
+      f[0] = lo(w << 12, 0xF000u);
+      f[1] = lo(w << 8, 0xF000u), f[2] = hi(w << 8, 0xF0000u);
+      f[3] = lo(w, 0xF000u), f[4] = hi(w, 0xF0000u);
+      f[5] = lo(w >> 8, 0xF000u), f[6] = hi(w >> 8, 0xF0000u);
+      f[7] = lo(w >> 16, 0xF000u);
+    }
     Row<T>::store(k + w.tok[r] * p.kts + h * p.khs + 8 * col, f);
-    const int sh = 4 * (2 * r + half);
+    const Affine val(half ? 128.0f : 2048.0f, sv[r], zv[r]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = code_value(words[i], sh, zv[r], sv[r]);
+    for (int i = 0; i < 8; ++i)  // nibbles 2 r and 2 r + 1 to bits 12 and 16
+      f[i] = val(r == 0 ? words[i] << 12 : r == 1 ? words[i] << 4 : words[i] >> (8 * r - 12),
+                 vmask);
     Row<T>::store(v + w.tok[r] * p.vts + h * p.vhs + 8 * col, f);
   }
 }
