@@ -467,8 +467,12 @@ __device__ __forceinline__ int own_length(const PrefixArgs& p, int b) {
 
 // CTAs 0 .. nprefix - 1: key range x row tile x KV head of the prefix (none
 // where the tcgen05 kernel takes it: nprefix is 0 here); the rest: key range x
-// KV head x sequence of the own tokens. Launched while the tcgen05 kernel still
-// runs, whose results the merge needs too: every CTA ends by waiting for it.
+// KV head x sequence of the own tokens. Bound by its instructions, about 640 a
+// warp's step of 32 keys, half of them dequantization: 64 sequences x 8 heads x 8
+// rows on 2000 to 2048 own tokens take 43 us (141 MB of cache, issue 51%, HBM 42%).
+// With few keys its latency is what counts: 4 chats on 1021 shared keys 8.6 us with
+// the merge. Launched while the tcgen05 kernel still runs, whose results the merge
+// needs too: every CTA ends by waiting for it.
 template <int NTP, int NTO>
 __global__ void __launch_bounds__(32 * kWarps, NTP * NTO == 1 ? 4 : 2)
     prefix_attn_kernel(const __grid_constant__ PrefixArgs p, int nprefix) {
@@ -589,9 +593,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 // Which kernel takes the prefix. On mma.sync the time grows with 16-row groups
 // times keys (45 ps each, the GPU full), on tcgen05 with row tiles times keys
 // (114 ps a key for 128 rows, 145 for 256) from about 10 us more. 8 KV heads,
-// mma.sync against tcgen05: 64 rows 14 and 16 us at 4096 keys, 30 and 27 at
-// 16384; 256 rows 22 and 24 us at 2048, 31 and 26 at 4096, 96 and 41 at 16384;
-// 32 rows 20 and 26 us at 16384, never the other way.
+// mma.sync against tcgen05: 64 rows 14 and 16 us at 4096 keys, 29 and 27 at
+// 16384; 256 rows 21 and 24 us at 2048, 30 and 27 at 4096, 91 and 42 at 16384;
+// 32 rows 19 and 26 us at 16384, 48 and 69 at 65536, never the other way.
 bool prefix_on_tc(int64_t Hkv, int64_t rows, int64_t P, int tiles, int groups_of_tiles) {
   const int64_t gain = 45 * ((rows + 15) / 16) - (tiles == 2 ? 145 : 114) * groups_of_tiles;
   return gain > 0 && Hkv * P > 10000000 / gain;

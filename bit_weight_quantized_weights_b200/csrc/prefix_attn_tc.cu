@@ -27,6 +27,13 @@
 // 7 bits of the scales, which makes them exact, and the rest multiplies the
 // score and the weight, two operations a weight.
 //
+// What bounds it: a tile of 256 rows x 128 keys takes about 4700 cycles, its MMAs
+// and its exponentials 2050 each, its 11200 warp instructions 2800 (softmax 5600,
+// dequantization 3100); a stream's scores, softmax and values follow one another and
+// two streams cover each other in part. 1024 rows x 8 heads x 65537 keys, with the
+// own tokens and the merge: 314 us with bf16 queries (877 TFLOP/s), 425 with fp16;
+// 512 x 8 x 32768: 104 us.
+//
 // MMAs of one issuing thread execute in order, so S of a tile completes after
 // the O += P V issued before it: when a softmax warp sees its scores it may
 // rescale its rows of O, and the next S may overwrite P.
