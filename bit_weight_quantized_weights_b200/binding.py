@@ -149,11 +149,8 @@ def _stream(stream=None):
 # microseconds on the GPU is launched from here, and the Stream objects of
 # torch.cuda.current_stream() cost as much as the launch.
 _current_device = torch.cuda.current_device
+_BF16, _F16, _I32, _U8 = torch.bfloat16, torch.float16, torch.int32, torch.uint8
 _raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _stream_on(dev, stream):
-    return stream.cuda_stream if stream is not None else _raw_stream(dev)
 
 
 def _cuda(t, dtype, name):
@@ -456,11 +453,12 @@ def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     """MXFP4 activations kept in 4 bits: x [M, K] (bf16, fp16 or fp32; rows may
     be strided) -> (planes uint8 [P, M, K/2], scale bytes uint8 [P, M, K/32])."""
     dev = _current_device()
-    dt, shape, xs = _DTYPES.get(x.dtype), x.shape, x.stride()
-    if dt is None or len(shape) != 2:
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or x.dim() != 2:
         raise ValueError("x must be a 2-D bfloat16, float16 or float32 tensor")
-    m, k = shape
-    if xs[1] != 1 and k > 1:
+    m, k = x.shape
+    ldx, inner = x.stride()
+    if inner != 1 and k > 1:
         raise ValueError("the rows of x must be contiguous")
     if planes is None:
         planes = x.new_empty((n_planes, m, k // 2), dtype=torch.uint8)
@@ -472,10 +470,13 @@ def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     elif scales.dtype is not torch.uint8 or scales.shape != (n_planes, m, k // 32) or \
             not scales.is_contiguous():
         raise ValueError("scales must be uint8 [%d, %d, %d]" % (n_planes, m, k // 32))
-    _on_device(dev, x, planes, scales)
-    _check(lib.wq_mx_quantize_planes(x.data_ptr(), dt, xs[0] if m > 1 else k, m, k, n_planes,
-                                     planes.data_ptr(), scales.data_ptr(),
-                                     _stream_on(dev, stream)), "wq_mx_quantize_planes")
+    if x.get_device() != dev or planes.get_device() != dev or scales.get_device() != dev:
+        _on_device(dev, x, planes, scales)
+    status = lib.wq_mx_quantize_planes(
+        x.data_ptr(), dt, ldx if m > 1 else k, m, k, n_planes, planes.data_ptr(),
+        scales.data_ptr(), _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise WqError(status, "wq_mx_quantize_planes")
     return planes, scales
 
 
@@ -489,29 +490,35 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
     tensor cores: planes and plane_scales as wq_mx_quantize_planes returns
     them, codes and scales as wq_mx_quantize packs the weights [N, K]."""
     dev = _current_device()
-    for t, name in ((planes, "planes"), (plane_scales, "plane_scales"), (codes, "codes"),
-                    (scales, "scales")):
-        if t.dtype is not torch.uint8 or not t.is_contiguous():
-            raise ValueError("%s must be uint8 and contiguous" % name)
-    shape = planes.shape
-    if len(shape) != 3:
+    if planes.dtype is not _U8 or plane_scales.dtype is not _U8 or codes.dtype is not _U8 or \
+            scales.dtype is not _U8 or not planes.is_contiguous() or \
+            not plane_scales.is_contiguous() or not codes.is_contiguous() or \
+            not scales.is_contiguous():
+        raise ValueError("planes, codes and their scales must be uint8 and contiguous")
+    if planes.dim() != 3:
         raise ValueError("planes must be [P, M, K/2]")
-    p, m, kh = shape
+    p, m, kh = planes.shape
     k = 2 * kh
     if plane_scales.shape != (p, m, k // 32) or codes.shape != (n, kh) or \
             scales.shape != (n, k // 32):
-        raise ValueError("scales or weights do not match planes %s and N = %d" % (tuple(shape), n))
+        raise ValueError("scales or weights do not match planes %s and N = %d"
+                         % (tuple(planes.shape), n))
     if workspace is None:
         workspace = mx_gemm_workspace(m, n, k, p, planes.device)
     if out is None:
         out = planes.new_empty((m, n), dtype=torch.bfloat16)
     elif out.dtype is not torch.bfloat16 or out.shape != (m, n) or not out.is_contiguous():
         raise ValueError("y must be bfloat16 [%d, %d], contiguous" % (m, n))
-    _on_device(dev, planes, plane_scales, codes, scales, workspace, out)
-    _check(lib.wq_mx_gemm(planes.data_ptr(), plane_scales.data_ptr(), m, n, k, p, codes.data_ptr(),
-                          scales.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), _stream_on(dev, stream)),
-           "wq_mx_gemm")
+    if planes.get_device() != dev or plane_scales.get_device() != dev or \
+            codes.get_device() != dev or scales.get_device() != dev or \
+            workspace.get_device() != dev or out.get_device() != dev:
+        _on_device(dev, planes, plane_scales, codes, scales, workspace, out)
+    status = lib.wq_mx_gemm(
+        planes.data_ptr(), plane_scales.data_ptr(), m, n, k, p, codes.data_ptr(),
+        scales.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise WqError(status, "wq_mx_gemm")
     return out
 
 
@@ -575,14 +582,13 @@ def _kv_cache(k_cache, v_cache, dev):
     kq, ks, kz = k_cache
     vq, vs, vz = v_cache
     shape = ks.shape
-    if len(shape) == 3 and kq.dtype is torch.int32 and vq.dtype is torch.int32 and \
-            ks.dtype is torch.float16 and kz.dtype is torch.float16 and \
-            vs.dtype is torch.float16 and vz.dtype is torch.float16 and kq.is_contiguous() and \
+    if kq.dtype is _I32 and vq.dtype is _I32 and ks.dtype is _F16 and kz.dtype is _F16 and \
+            vs.dtype is _F16 and vz.dtype is _F16 and kq.is_contiguous() and \
             vq.is_contiguous() and ks.is_contiguous() and kz.is_contiguous() and \
             vs.is_contiguous() and vz.is_contiguous() and kz.shape == shape and \
             vs.shape == shape and vz.shape == shape and kq.get_device() == dev and \
             vq.get_device() == dev and ks.get_device() == dev and kz.get_device() == dev and \
-            vs.get_device() == dev and vz.get_device() == dev:
+            vs.get_device() == dev and vz.get_device() == dev and len(shape) == 3:
         b, hkv, cap = shape
         d = vq.shape[-1]
         if kq.shape == (b, hkv, cap, d // 8) and vq.shape == (b, hkv, (cap + 7) // 8, d):
@@ -614,23 +620,30 @@ _Strides = ctypes.c_int64 * 2
 def _kv_rows(k, v, cache, starts, offsets, dev):
     """Check packed rows [T, Hkv, D] against a cache: (T, dtype, strides of k and v)."""
     b, hkv, _, d = cache
-    shape, dt = k.shape, _DTYPES.get(k.dtype)
-    if dt is None or v.dtype is not k.dtype:
+    shape, kind = k.shape, k.dtype
+    dt = _DTYPES.get(kind)
+    if dt is None or v.dtype is not kind:
         raise ValueError("k and v must both be bfloat16, float16 or float32")
-    if v.shape != shape or len(shape) != 3 or shape[1] != hkv or shape[2] != d:
+    t = shape[0] if len(shape) == 3 else -1
+    if shape != (t, hkv, d) or v.shape != shape:
         raise ValueError("k and v must be [T, %d, %d], got %s and %s"
                          % (hkv, d, tuple(shape), tuple(v.shape)))
-    ks, vs = k.stride(), v.stride()
-    if ks[2] != 1 or vs[2] != 1:
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if k2 != 1 or v2 != 1:
         raise ValueError("the last dimension of k and v must be contiguous")
-    if starts.dtype is not torch.int32 or offsets.dtype is not torch.int32 or \
+    if starts.dtype is not _I32 or offsets.dtype is not _I32 or \
             starts.shape != (b,) or offsets.shape != (b + 1,) or \
             not starts.is_contiguous() or not offsets.is_contiguous():
         raise ValueError("starts must be int32 [%d] and offsets int32 [%d], contiguous" % (b, b + 1))
-    _on_device(dev, k, v, starts, offsets)
-    if shape[0] == 1 or hkv == 1:  # the stride of one element means nothing
-        ks, vs = ((s[0] if shape[0] > 1 else 0, s[1] if hkv > 1 else 0) for s in (ks, vs))
-    return shape[0], dt, _Strides(ks[0], ks[1]), _Strides(vs[0], vs[1])
+    if k.get_device() != dev or v.get_device() != dev or starts.get_device() != dev or \
+            offsets.get_device() != dev:
+        _on_device(dev, k, v, starts, offsets)
+    if t == 1:  # the stride of one element means nothing
+        k0 = v0 = 0
+    if hkv == 1:
+        k1 = v1 = 0
+    return t, dt, _Strides(k0, k1), _Strides(v0, v1)
 
 
 def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
@@ -642,11 +655,15 @@ def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
     dev = _current_device()
     b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     t, dt, ks, vs = _kv_rows(k, v, cache, starts, offsets, dev)
-    _check(lib.wq_kv_append(k.data_ptr(), v.data_ptr(), dt, t, hkv, d, ks, vs, b,
-                            starts.data_ptr(), offsets.data_ptr(), cap,
-                            k_cache[0].data_ptr(), k_cache[1].data_ptr(), k_cache[2].data_ptr(),
-                            v_cache[0].data_ptr(), v_cache[1].data_ptr(), v_cache[2].data_ptr(),
-                            _stream_on(dev, stream)), "wq_kv_append")
+    kq, kscale, kzero = k_cache
+    vq, vscale, vzero = v_cache
+    status = lib.wq_kv_append(
+        k.data_ptr(), v.data_ptr(), dt, t, hkv, d, ks, vs, b, starts.data_ptr(),
+        offsets.data_ptr(), cap, kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(),
+        vq.data_ptr(), vscale.data_ptr(), vzero.data_ptr(),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise WqError(status, "wq_kv_append")
 
 
 def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k_out=None,
@@ -665,11 +682,15 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
     t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets, dev)
     if t != total:
         raise ValueError("k_out and v_out must have %d rows" % total)
-    _check(lib.wq_kv_read(k_cache[0].data_ptr(), k_cache[1].data_ptr(), k_cache[2].data_ptr(),
-                          v_cache[0].data_ptr(), v_cache[1].data_ptr(), v_cache[2].data_ptr(),
-                          b, hkv, d, cap, starts.data_ptr(), offsets.data_ptr(), t,
-                          k_out.data_ptr(), v_out.data_ptr(), dt, ks, vs,
-                          _stream_on(dev, stream)), "wq_kv_read")
+    kq, kscale, kzero = k_cache
+    vq, vscale, vzero = v_cache
+    status = lib.wq_kv_read(
+        kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(), vscale.data_ptr(),
+        vzero.data_ptr(), b, hkv, d, cap, starts.data_ptr(), offsets.data_ptr(), t,
+        k_out.data_ptr(), v_out.data_ptr(), dt, ks, vs,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise WqError(status, "wq_kv_read")
     return k_out, v_out
 
 
@@ -692,41 +713,49 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
     prefix_k = prefix_v = None: no prefix."""
     dev = _current_device()
     b, hkv, cap, d = _kv_cache(k_cache, v_cache, dev)
-    shape, dtype, qs = q.shape, q.dtype, q.stride()
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError("q must be bfloat16 or float16, got %s" % dtype)
-    if len(shape) != 3 or shape[0] != b or shape[2] != d:
+    shape, kind = q.shape, q.dtype
+    if kind is not _BF16 and kind is not _F16:
+        raise ValueError("q must be bfloat16 or float16, got %s" % kind)
+    hq = shape[1] if len(shape) == 3 else 0
+    if shape != (b, hq, d):
         raise ValueError("q must be [%d, Hq, %d], got %s" % (b, d, tuple(shape)))
-    hq = shape[1]
-    if qs[2] != 1 or (hq > 1 and qs[1] != d):
+    q0, q1, q2 = q.stride()
+    if q2 != 1 or (hq > 1 and q1 != d):
         raise ValueError("the heads of q must be contiguous")
-    if lengths.dtype is not torch.int32 or lengths.shape != (b,) or not lengths.is_contiguous():
+    if lengths.dtype is not _I32 or lengths.shape != (b,) or not lengths.is_contiguous():
         raise ValueError("lengths must be int32 [%d], contiguous" % b)
     if prefix_k is None and prefix_v is None:
         pre = (None,) * 6
         pcap, prefix_len = 0, 0
     else:
         one, ph, pcap, pd = _kv_cache(prefix_k, prefix_v, dev)
-        if (one, ph, pd) != (1, hkv, d):
+        if one != 1 or ph != hkv or pd != d:
             raise ValueError("the prefix cache must be [1, %d, capacity, ...] with D = %d" % (hkv, d))
-        prefix_len = pcap if prefix_len is None else prefix_len
-        pre = (prefix_k[0].data_ptr(), prefix_k[1].data_ptr(), prefix_k[2].data_ptr(),
-               prefix_v[0].data_ptr(), prefix_v[1].data_ptr(), prefix_v[2].data_ptr())
+        if prefix_len is None:
+            prefix_len = pcap
+        kq, kscale, kzero = prefix_k
+        vq, vscale, vzero = prefix_v
+        pre = (kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(),
+               vscale.data_ptr(), vzero.data_ptr())
     if workspace is None:
         workspace = prefix_attention_workspace(b, hq, hkv, prefix_len, cap, d, q.device)
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
-    elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
+    elif out.dtype is not kind or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must have q's type and shape, contiguous")
-    _on_device(dev, q, lengths, workspace, out)
-    _check(lib.wq_prefix_attention(q.data_ptr(), _DTYPES[dtype], qs[0] if b > 1 else hq * d, b, hq,
-                                   hkv, d, prefix_len, pcap, *pre, cap,
-                                   k_cache[0].data_ptr(), k_cache[1].data_ptr(),
-                                   k_cache[2].data_ptr(), v_cache[0].data_ptr(),
-                                   v_cache[1].data_ptr(), v_cache[2].data_ptr(),
-                                   lengths.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(),
-                                   _stream_on(dev, stream)), "wq_prefix_attention")
+    if q.get_device() != dev or lengths.get_device() != dev or \
+            workspace.get_device() != dev or out.get_device() != dev:
+        _on_device(dev, q, lengths, workspace, out)
+    kq, kscale, kzero = k_cache
+    vq, vscale, vzero = v_cache
+    status = lib.wq_prefix_attention(
+        q.data_ptr(), _DTYPES[kind], q0 if b > 1 else hq * d, b, hq, hkv, d, prefix_len, pcap,
+        *pre, cap, kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(),
+        vscale.data_ptr(), vzero.data_ptr(), lengths.data_ptr(), out.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        raise WqError(status, "wq_prefix_attention")
     return out
 
 
