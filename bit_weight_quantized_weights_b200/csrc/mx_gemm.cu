@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 //                of TMEM columns (every warp writes its lane quarter: the MMA
 //                reads the scales from all four). tcgen05.cp from shared memory
 //                by the MMA's thread took a fifth of the MMAs' time.
+//                Small products load the bytes as given, a row a thread.
 //   warps 8-15   epilogue: TMEM to registers as packed bf16, which frees the
 //                accumulator for the next tile, then through shared memory to
 //                TMA stores (rows of 128 bytes; one 16-byte store a token cost
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 // CTAs are persistent and take every gridDim.x-th tile. 8192 x 14336 x 4096 with two
 // planes: 325 us with the scale pass, 5.9 POP/s, the tensor cores busy 81% of the
 // cycles (bare MMAs: 6.7 POP/s at the same power); with one plane 197 us, bound by
-// the operands' way from L2; 33 x 4096 x 4096 9.3 us, bound by latency.
+// the operands' way from L2; 33 x 4096 x 4096 9.0 us, bound by latency.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128;
 constexpr int kBKBytes = 128;   // bytes of a stage's row: 256 k
@@ -298,12 +299,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const u
 
 struct MxArgs {
   const uint8_t* sf;  // scale pieces of the token blocks (by plane), then of the weights
+  const uint8_t *xs, *ws;  // the scales as given (kDirect)
   int M, N, K;
   int mt, tiles;      // token tiles; all tiles
   int xrows;          // token rows a TMA load brings: 128, or M rounded up to 8
 };
 
-template <int BN, int PL>
+template <int BN, int PL, bool kDirect>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x,
                    const __grid_constant__ CUtensorMap tmap_w,
@@ -429,6 +431,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (sm100::elect_one()) sm100::mma_commit(mma_done);
     __syncwarp();
+  } else if (kDirect && warp >= 4 && warp < 8) {
+    // ---------------- scales as they are given: one tile a CTA ----------------
+    // Thread = row of every operand; the rows' words meet in shared memory (the
+    // epilogue's buffers, which are free until the tile is complete).
+    constexpr int D = Cfg::kSfAhead, kOps = PL + 1;
+    static_assert(!kDirect || (Cfg::kWPieces == 1 && 2 * kOps * 1024 <= Cfg::kOutBytes),
+                  "one block of features, two stages of pieces");
+    const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
+    const int r = 32 * (warp & 3) + lane, words = a.K / 128;
+    const uint32_t* src[kOps];  // null: no such row, or features past the tile
+#pragma unroll
+    for (int o = 0; o < kOps; ++o) {
+      const int row = o < PL ? (blockIdx.x % a.mt) * kBM + r : (int)(blockIdx.x / a.mt) * BN + r;
+      const bool in = o < PL ? row < a.M : row < a.N && r < BN;
+      const uint8_t* base = o < PL ? a.xs + (int64_t)o * a.M * (a.K / 32) : a.ws;
+      src[o] = in ? reinterpret_cast<const uint32_t*>(base + (int64_t)row * (a.K / 32)) : nullptr;
+    }
+    const bool pairs = (words & 1) == 0;  // K % 256 == 0: a stage's two words are aligned
+    auto load = [&](uint32_t (&v)[kOps][2], int kt) {
+#pragma unroll
+      for (int o = 0; o < kOps; ++o) {
+        if (pairs) {
+          const uint2 w = src[o] ? *reinterpret_cast<const uint2*>(src[o] + 2 * kt)
+                                 : make_uint2(0u, 0u);
+          v[o][0] = w.x, v[o][1] = w.y;
+        } else {
+          v[o][0] = src[o] ? src[o][2 * kt] : 0u;
+          v[o][1] = src[o] && 2 * kt + 1 < words ? src[o][2 * kt + 1] : 0u;
+        }
+      }
+    };
+    uint32_t v[D][kOps][2];
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (d < KT) load(v[d], d);
+    bool ok = true;  // (after an abort the warps still meet at every stage's barrier)
+    for (int base = 0; base < KT; base += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        const int it = base + d;
+        if (it >= KT) break;
+        uint32_t* buf = reinterpret_cast<uint32_t*>(sout + (it & 1) * kOps * 1024);
+#pragma unroll
+        for (int o = 0; o < kOps; ++o)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) buf[(2 * o + g) * 128 + 4 * lane + (warp & 3)] = v[d][o][g];
+        if (it + D < KT) load(v[d], it + D);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int f = it % S;
+        if (ok && it >= S)
+          ok = __all_sync(0xffffffffu,
+                          sm100::mbar_wait(&empty[f], (uint32_t)(it / S - 1) & 1u,
+                                           &g_mx_gemm_error, 0x3301u, abort_flag, wc.limit_ns));
+        if (ok) {
+          sm100::tc_fence_after();
+          const uint4* piece = reinterpret_cast<const uint4*>(buf) + lane;
+#pragma unroll
+          for (int o = 0; o < kOps; ++o)
+            tmem_st8(tmem_sf + quarter + (uint32_t)(f * Cfg::kSfCols + 8 * o), piece[64 * o],
+                     piece[64 * o + 32]);
+          sm100::tmem_st_wait();
+          sm100::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&sffull[f]);
+        }
+      }
+    }
   } else if (warp >= 4 && warp < 8) {
     // ---------------- scales ----------------
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are complete
@@ -587,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) sm100::tmem_dealloc(tmem, Cfg::kTmemCols);
 }
 
-template <int BN, int PL>
+template <int BN, int PL, bool kDirect>
 wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a0,
                         cudaStream_t st) {
   using Cfg = MxCfg<BN, PL>;
@@ -600,7 +669,7 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, cons
                     (uint64_t)a0.N, (uint64_t)a0.K / 2, kBKBytes, BN, CU_TENSOR_MAP_SWIZZLE_128B))
     return WQ_ERR_CUDA;
   static std::atomic<uint64_t> smem_set{0};
-  if (!allow_smem(mx_gemm_kernel<BN, PL>, Cfg::kSmem, smem_set)) return WQ_ERR_CUDA;
+  if (!allow_smem(mx_gemm_kernel<BN, PL, kDirect>, Cfg::kSmem, smem_set)) return WQ_ERR_CUDA;
   MxArgs a = a0;
   a.tiles = a.mt * ((a.N + BN - 1) / BN);
   cudaLaunchConfig_t cfg = {};
@@ -608,19 +677,37 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, cons
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = kDirect ? 0 : 1;  // (the scale pass is what it may overlap)
   cfg.stream = st;
   cfg.gridDim = dim3((unsigned)std::min(a.tiles, num_sms()), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmem;
-  if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, PL>, tx, tw, ty, a, wait_ctl()) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, PL, kDirect>, tx, tw, ty, a, wait_ctl()) != cudaSuccess)
     return WQ_ERR_CUDA;
   return launch_status();
 }
 
+template <int BN, int PL>
+wq_status launch_width(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a,
+                       const ScaleArgs& sa, cudaStream_t st) {
+  // Few rows of scales a stage, and a tile a CTA: the product takes them as they are
+  // and the pass is saved. Two planes, K = 4096, with the pass and without: 33 tokens
+  // x 4096 features 9.8 and 9.2 us, 64 9.5 and 9.5, 96 9.6 and 10.5, 33 x 14336 11.6
+  // and 11.2, 64 11.7 and 12.6; one plane: 33 x 4096 8.7 and 7.3, 128 8.9 and 8.3, 128 x
+  // 14336 10.4 and 11.3.
+  if constexpr (BN <= 128) {
+    const int64_t tiles = (int64_t)a.mt * ((a.N + BN - 1) / BN);
+    if (tiles <= num_sms() && PL * std::min(a.M, kBM) + BN <= 176)
+      return launch_gemm_t<BN, PL, true>(tx, wcodes, y, a, st);
+  }
+  const int64_t blocks = (int64_t)PL * a.mt + (a.N + 127) / 128;
+  mx_scales_kernel<<<(unsigned)(blocks * sa.chunks), 256, 0, st>>>(sa);
+  return launch_gemm_t<BN, PL, false>(tx, wcodes, y, a, st);
+}
+
 template <int PL>
 wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a,
-                      cudaStream_t st) {
+                      const ScaleArgs& sa, cudaStream_t st) {
   // the tile width with the least time for the slowest CTA: whole tiles an SM
   // takes, times a tile's cost
   const int64_t mt = a.mt, sms = num_sms();
@@ -629,10 +716,10 @@ wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const 
     return (tiles + sms - 1) / sms * tile;
   };
   const int64_t c32 = cost(32, 70), c64 = cost(64, 90), c128 = cost(128, 140), c256 = cost(256, 256);
-  if (c256 <= std::min({c128, c64, c32})) return launch_gemm_t<256, PL>(tx, wcodes, y, a, st);
-  if (c128 <= std::min(c64, c32)) return launch_gemm_t<128, PL>(tx, wcodes, y, a, st);
-  if (c64 <= c32) return launch_gemm_t<64, PL>(tx, wcodes, y, a, st);
-  return launch_gemm_t<32, PL>(tx, wcodes, y, a, st);
+  if (c256 <= std::min({c128, c64, c32})) return launch_width<256, PL>(tx, wcodes, y, a, sa, st);
+  if (c128 <= std::min(c64, c32)) return launch_width<128, PL>(tx, wcodes, y, a, sa, st);
+  if (c64 <= c32) return launch_width<64, PL>(tx, wcodes, y, a, sa, st);
+  return launch_width<32, PL>(tx, wcodes, y, a, sa, st);
 }
 
 template <typename T>
@@ -686,17 +773,17 @@ wq_status launch_mx_gemm(const uint8_t* xc, const uint8_t* xs, int64_t M, int64_
   sa.xblocks = (int)((M + 127) / 128);
   sa.kt = (int)((K + 255) / 256);
   sa.chunks = (2 * sa.kt + 7) / 8;
-  const int64_t blocks = (int64_t)P * sa.xblocks + (N + 127) / 128;
-  mx_scales_kernel<<<(unsigned)(blocks * sa.chunks), 256, 0, st>>>(sa);
   MxArgs a;
   a.sf = sa.out;
+  a.xs = xs;
+  a.ws = ws;
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;
   a.mt = sa.xblocks;
   a.tiles = 0;
   a.xrows = xrows;
-  return P == 1 ? launch_gemm<1>(tx, wc, y, a, st) : launch_gemm<2>(tx, wc, y, a, st);
+  return P == 1 ? launch_gemm<1>(tx, wc, y, a, sa, st) : launch_gemm<2>(tx, wc, y, a, sa, st);
 }
 
 wq_status read_mx_gemm_error(bool clear, uint32_t* v) {

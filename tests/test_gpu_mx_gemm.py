@@ -129,6 +129,18 @@ def test_product(wq, m, n, k, planes):
     _check(y, hat, w, planes)
 
 
+# Around the rule for scales taken without a pass: few rows, a tile a CTA, K past
+# the ring of stages, K % 256 = 128, the last tile of features cut.
+EDGES = [(20, 4736, 1152), (20, 4752, 1152), (72, 1040, 2176), (73, 1040, 2176), (128, 528, 4352),
+         (144, 2048, 640), (160, 80, 4224)]
+
+
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("m,n,k", EDGES)
+def test_product_with_and_without_the_scale_pass(wq, m, n, k, planes):
+    test_product(wq, m, n, k, planes)
+
+
 @pytest.mark.parametrize("m", [64, 400])
 def test_every_code_and_scale_lands(wq, m):
     """Random codes and widely spread scale bytes: a scale taken for the wrong
@@ -214,10 +226,10 @@ def test_empty_and_refusals(wq):
         wq.wq_mx_gemm(p3, s3, 32, codes[:, :48].contiguous(), scales[:, :3].contiguous())
 
 
-def test_bounded_wait_expires_cleanly(wq):
+@pytest.mark.parametrize("m,n,k", [(200, 512, 1024), (20, 512, 4352)])
+def test_bounded_wait_expires_cleanly(wq, m, n, k):
     """With the loader's first k-tile withheld the kernel gives up, reports the
     wait and returns; the next call is right."""
-    m, n, k = 200, 512, 1024
     x = _x(m, k)
     codes, scales, w = _weights(wq, n, k)
     xc, xs = wq.wq_mx_quantize_planes(x.cuda(), 2)
