@@ -123,3 +123,55 @@ def test_attention_block_decodes(wq, b, hq, hkv, planes):
         want, mag = _linear(attn.view(b, hq * D).double().cpu().numpy(), weights[1][2], planes)
         _close_bf16(y, want, planes * hq * D / 32 * 2.0 ** -23 * mag)
     assert wq.wq_device_error()[0] == wq.WQ_OK
+
+
+def test_operators_on_two_streams_at_once(wq):
+    """The same calls on two streams that run together, each with its own
+    workspace and outputs, give what they give one after the other."""
+    g = torch.Generator().manual_seed(21)
+    b, hq, hkv, p, cap = 24, 16, 2, 3000, 40
+    q = torch.randn(b, hq, D, generator=g).bfloat16().cuda()
+    prompt, own = wq.kv_cache_alloc(1, hkv, p), wq.kv_cache_alloc(b, hkv, cap)
+    rows = [torch.randn(n, hkv, D, generator=g).bfloat16().cuda() for n in (p, p, b * 30, b * 30)]
+    i32 = lambda v: torch.tensor(list(v), dtype=torch.int32, device="cuda")
+    wq.wq_kv_append(*rows[:2], *prompt, i32([0]), i32([0, p]))
+    starts, edges, lengths = i32([0] * b), i32(range(0, 30 * b + 1, 30)), i32([30] * b)
+    wq.wq_kv_append(*rows[2:], *own, starts, edges)
+    x = torch.randn(300, 1024, generator=g).bfloat16().cuda()
+    wc, ws = wq.wq_mx_quantize((torch.randn(2048, 1024, generator=g) * 0.02).cuda())
+
+    def step(work):
+        planes, scales = wq.wq_mx_quantize_planes(x, 2)
+        y = wq.wq_mx_gemm(planes, scales, 2048, wc, ws, workspace=work[0])
+        small = wq.wq_mx_gemm(planes[:, :20].contiguous(), scales[:, :20].contiguous(), 2048, wc,
+                              ws, workspace=work[1])
+        outs = []
+        for path in (1, 2):
+            wq.wq_test_set_prefix_path(path)
+            outs.append(wq.wq_prefix_attention(q, *prompt, *own, lengths, workspace=work[2]))
+        return [y, small, *outs, *wq.wq_kv_read(*own, starts, edges, 30 * b)]
+
+    def workspaces():
+        sizes = []
+        for path in (1, 2):
+            wq.wq_test_set_prefix_path(path)
+            sizes.append(wq.prefix_attention_workspace(b, hq, hkv, p, cap).numel())
+        return (wq.mx_gemm_workspace(300, 2048, 1024), wq.mx_gemm_workspace(20, 2048, 1024),
+                torch.empty(max(sizes), dtype=torch.uint8, device="cuda"))
+
+    try:
+        work = [workspaces(), workspaces()]
+        want = step(work[0])
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        got = [[], []]
+        for _ in range(10):
+            for i, stream in enumerate(streams):
+                with torch.cuda.stream(stream):
+                    got[i].append(step(work[i]))
+        torch.cuda.synchronize()
+    finally:
+        wq.wq_test_set_prefix_path(0)
+    assert wq.wq_device_error()[0] == wq.WQ_OK
+    for outs in got[0] + got[1]:
+        assert all(torch.equal(a, c) for a, c in zip(outs, want))
