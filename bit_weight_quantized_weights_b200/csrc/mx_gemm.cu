@@ -12,8 +12,11 @@
 //   y[m, n] = sum_p sum_blk 2^(e_p + e_w) sum_{k in blk} x_p[m, k] w[n, k].
 // One plane is the plain MXFP4 product.
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "sm100.cuh"
+#include "splitk_common.cuh"
 
 namespace wq {
 
@@ -232,10 +235,11 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 //                accumulator for the next tile, then through shared memory to
 //                TMA stores (rows of 128 bytes; one 16-byte store a token cost
 //                70 us of 350 at 8192 x 14336 x 4096)
-// CTAs are persistent and take every gridDim.x-th tile. 8192 x 14336 x 4096 with two
+// CTAs are persistent and take every gridDim.x-th tile; where there are few tiles and
+// a long K, the 2 or 4 CTAs of a cluster share a tile's K. 8192 x 14336 x 4096 with two
 // planes: 325 us with the scale pass, 5.9 POP/s, the tensor cores busy 81% of the
 // cycles (bare MMAs: 6.7 POP/s at the same power); with one plane 197 us, bound by
-// the operands' way from L2; 33 x 4096 x 4096 9.0 us, bound by latency.
+// the operands' way from L2; 33 x 4096 x 4096 7.5 us, bound by latency.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128;
 constexpr int kBKBytes = 128;   // bytes of a stage's row: 256 k
@@ -303,6 +307,8 @@ struct MxArgs {
   int M, N, K;
   int mt, tiles;      // token tiles; all tiles
   int xrows;          // token rows a TMA load brings: 128, or M rounded up to 8
+  int split;          // log2 of the CTAs that share a tile's K (above 0: one tile a CTA)
+  uint16_t* y;
 };
 
 template <int BN, int PL, bool kDirect>
@@ -329,6 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KT = (a.K / 2 + kBKBytes - 1) / kBKBytes;
+  // this CTA's first tile, and its stages [k0, k0 + KL) of every tile
+  constexpr bool kSplits = BN == 64 || BN == 128;  // the widths that share K
+  const int split = kSplits ? a.split : 0;
+  const int rank = (int)blockIdx.x & ((1 << split) - 1);  // (clusters start at multiples)
+  const int tile0 = (int)blockIdx.x >> split, tstep = (int)gridDim.x >> split;
+  const int k0 = rank * KT >> split, KL = ((rank + 1) * KT >> split) - k0;
 
   if (threadIdx.x == 0) {
     sm100::tma_prefetch_desc(&tmap_x);
@@ -360,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0;
     bool ok = true;
     const uint32_t bytes = (uint32_t)(PL * a.xrows * kBKBytes) + Cfg::kWBytes;
-    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+    for (int t = tile0; t < a.tiles && ok; t += tstep) {
       const int m0 = (t % a.mt) * kBM, n0 = (t / a.mt) * BN;
-      for (int kt = 0; kt < KT; ++kt, ++it) {
+      for (int kt = k0; kt < k0 + KL; ++kt, ++it) {
         const int s = it % S;
         if (it >= S) {
           ok = __all_sync(0xffffffffu,
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = sm100::uniform(tmem), acc = tm + (uint32_t)(who * BN);
     int it0 = 0, n = 0;  // the tile's first stage; the tile
     bool ok = true;
-    for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x, ++n, it0 += KT) {
+    for (int t = tile0; t < a.tiles && ok; t += tstep, ++n, it0 += KL) {
       if (n > 0) {
         ok = __all_sync(0xffffffffu,
                         sm100::mbar_wait(acc_empty, (uint32_t)(n - 1) & 1u, &g_mx_gemm_error,
@@ -398,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         sm100::tc_fence_after();
       }
-      for (int kt = who; kt < KT; kt += Cfg::kIssuers) {
+      for (int kt = who; kt < KL; kt += Cfg::kIssuers) {
         const int it = it0 + kt, s = it % S;
         const uint32_t ph = (uint32_t)(it / S) & 1u;
         ok = __all_sync(0xffffffffu, sm100::mbar_wait(&full[s], ph, &g_mx_gemm_error, 0x3202u,
@@ -443,13 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t* src[kOps];  // null: no such row, or features past the tile
 #pragma unroll
     for (int o = 0; o < kOps; ++o) {
-      const int row = o < PL ? (blockIdx.x % a.mt) * kBM + r : (int)(blockIdx.x / a.mt) * BN + r;
+      const int row = o < PL ? (tile0 % a.mt) * kBM + r : tile0 / a.mt * BN + r;
       const bool in = o < PL ? row < a.M : row < a.N && r < BN;
       const uint8_t* base = o < PL ? a.xs + (int64_t)o * a.M * (a.K / 32) : a.ws;
       src[o] = in ? reinterpret_cast<const uint32_t*>(base + (int64_t)row * (a.K / 32)) : nullptr;
     }
     const bool pairs = (words & 1) == 0;  // K % 256 == 0: a stage's two words are aligned
-    auto load = [&](uint32_t (&v)[kOps][2], int kt) {
+    auto load = [&](uint32_t (&v)[kOps][2], int it) {
+      const int kt = k0 + it;
 #pragma unroll
       for (int o = 0; o < kOps; ++o) {
         if (pairs) {
@@ -465,19 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t v[D][kOps][2];
 #pragma unroll
     for (int d = 0; d < D; ++d)
-      if (d < KT) load(v[d], d);
+      if (d < KL) load(v[d], d);
     bool ok = true;  // (after an abort the warps still meet at every stage's barrier)
-    for (int base = 0; base < KT; base += D) {
+    for (int base = 0; base < KL; base += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         const int it = base + d;
-        if (it >= KT) break;
+        if (it >= KL) break;
         uint32_t* buf = reinterpret_cast<uint32_t*>(sout + (it & 1) * kOps * 1024);
 #pragma unroll
         for (int o = 0; o < kOps; ++o)
 #pragma unroll
           for (int g = 0; g < 2; ++g) buf[(2 * o + g) * 128 + 4 * lane + (warp & 3)] = v[d][o][g];
-        if (it + D < KT) load(v[d], it + D);
+        if (it + D < KL) load(v[d], it + D);
         asm volatile("bar.sync 1, 128;" ::: "memory");
         const int f = it % S;
         if (ok && it >= S)
@@ -506,20 +519,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the pieces of one stage in column order: planes (2 of k each), then the
     // weights' by k. They are 1024 bytes (2 pieces) after the stage before's.
     constexpr int D = Cfg::kSfAhead;
-    const int mine = blockIdx.x < a.tiles ? (a.tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-    const int total = mine * KT;  // stages of this CTA
+    const int mine = tile0 < a.tiles ? (a.tiles - 1 - tile0) / tstep + 1 : 0;
+    const int total = mine * KL;  // stages of this CTA
     const uint8_t *px[PL], *pw[Cfg::kWPieces];
-    int lt = blockIdx.x, lk = 0;  // the next stage to load
+    int lt = tile0, lk = 0;  // the next stage to load
     auto next = [&](uint4 (&v)[kPieces]) {
       if (lk == 0) {
         const int mb = lt % a.mt, n0 = (lt / a.mt) * BN;
 #pragma unroll
         for (int p = 0; p < PL; ++p)
-          px[p] = a.sf + (int64_t)(p * a.mt + mb) * KT * 1024 + 16 * lane;
+          px[p] = a.sf + ((int64_t)(p * a.mt + mb) * KT + k0) * 1024 + 16 * lane;
 #pragma unroll
         for (int w = 0; w < Cfg::kWPieces; ++w)
           // a block of 128 features past N has no pieces: its columns are not stored
-          pw[w] = a.sf + (int64_t)(PL * a.mt + min(n0 / 128 + w, (a.N - 1) / 128)) * KT * 1024 +
+          pw[w] = a.sf +
+                  ((int64_t)(PL * a.mt + min(n0 / 128 + w, (a.N - 1) / 128)) * KT + k0) * 1024 +
                   16 * lane;
       }
 #pragma unroll
@@ -533,9 +547,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int p = 0; p < PL; ++p) px[p] += 1024;
 #pragma unroll
       for (int w = 0; w < Cfg::kWPieces; ++w) pw[w] += 1024;
-      if (++lk == KT) {
+      if (++lk == KL) {
         lk = 0;
-        lt += gridDim.x;
+        lt += tstep;
       }
     };
     uint4 v[D][kPieces];
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int d = 0; d < D; ++d)
       if (d < total) next(v[d]);
     bool ok = true;
-    int st = blockIdx.x, sk = 0, c = 0;  // the stage being stored
+    int st = tile0, sk = 0, c = 0;  // the stage being stored
     for (int base = 0; base < total && ok; base += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
@@ -567,9 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c & 2) v[d][i] = make_uint4(v[d][i].z, v[d][i].w, 0u, 0u);
             if (c & 1) v[d][i].x = v[d][i].y;
           }
-          if (++sk == KT) {
+          if (++sk == KL) {
             sk = 0;
-            st += gridDim.x;
+            st += tstep;
           }
         }
 #pragma unroll
@@ -582,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) sm100::mbar_arrive(&sffull[f]);
       }
     }
-  } else if (warp >= 8 && warp < 8 + Cfg::kEpiWarps) {
+  } else if (split == 0 && warp >= 8 && warp < 8 + Cfg::kEpiWarps) {
     // ---------------- epilogue: thread = token, kEpiCols of the tile's features ----------------
     const int q = warp & 3, part = (warp - 8) >> 2;
     constexpr int kCols = Cfg::kEpiCols;
     uint8_t* buf = sout + (warp - 8) * Cfg::kStageOut;
     int n = 0;
-    for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n) {
+    for (int t = tile0; t < a.tiles; t += tstep, ++n) {
       const int m0 = (t % a.mt) * kBM + 32 * q;
       const int col0 = (t / a.mt) * BN + part * kCols;
       const bool got = sm100::mbar_wait(acc_full, (uint32_t)n & 1u, &g_mx_gemm_error, 0x3401u,
@@ -601,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[32];
         sm100::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + part * kCols + 32 * c, v);
         sm100::tmem_ld_wait();
-        if (Cfg::kIssuers == 2 && KT > 1) {
+        if (Cfg::kIssuers == 2 && KL > 1) {
           uint32_t u[32];
           sm100::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + BN + part * kCols + 32 * c, u);
           sm100::tmem_ld_wait();
@@ -641,6 +655,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) sm100::bulk_wait_all();
   }
 
+  // ---------------- a tile's K over the cluster ----------------
+  // Every rank leaves its sums in its own stages (free by then), [row][BN] fp32 with
+  // 16-byte piece i of a row at i ^ (row % 8) within 128 bytes; rank r adds the tile's
+  // columns [r BN / C, (r + 1) BN / C) of all C ranks, in their order, and stores them.
+  if (kSplits && split > 0) {
+    const int m0 = (tile0 % a.mt) * kBM, n0 = tile0 / a.mt * BN;
+    const int rows = min(kBM, a.M - m0);
+    auto place = [](int row, int piece) {
+      return (uint32_t)(row * BN * 4 + ((piece ^ (row & 7)) << 4));
+    };
+    if (warp >= 8 && warp < 8 + Cfg::kEpiWarps) {
+      const int q = warp & 3, part = (warp - 8) >> 2, row = 32 * q + lane;
+      const bool got = __all_sync(
+          0xffffffffu, sm100::mbar_wait(acc_full, 0u, &g_mx_gemm_error, 0x3402u, abort_flag,
+                                        wc.limit_ns));
+      sm100::tc_fence_after();
+      if (got && 32 * q < rows) {
+#pragma unroll
+        for (int c = 0; c < Cfg::kEpiCols / 32; ++c) {
+          const int col = part * Cfg::kEpiCols + 32 * c;
+          const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)col;
+          uint32_t v[32];
+          sm100::tmem_ld32(at, v);
+          sm100::tmem_ld_wait();
+          if (Cfg::kIssuers == 2 && KL > 1) {
+            uint32_t u[32];
+            sm100::tmem_ld32(at + BN, u);
+            sm100::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(smem + place(row, col / 4 + i)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    }
+    __syncwarp();
+    splitk::cluster_sync_all();
+    auto finish = [&](auto ranks) {
+      constexpr int C = decltype(ranks)::value;
+      constexpr int kGroups = BN / C / 8;  // of 8 columns, a thread each
+      uint32_t src[C];
+#pragma unroll
+      for (int r = 0; r < C; ++r) src[r] = splitk::map_rank(smem, (uint32_t)r);
+      for (int u = threadIdx.x; u < rows * kGroups; u += kThreads) {
+        const int row = u / kGroups, col = rank * (BN / C) + u % kGroups * 8;
+        if (n0 + col >= a.N) continue;
+        float4 x[C][2];
+#pragma unroll
+        for (int r = 0; r < C; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(x[r][h].x), "=f"(x[r][h].y), "=f"(x[r][h].z), "=f"(x[r][h].w)
+                         : "r"(src[r] + place(row, col / 4 + h)));
+#pragma unroll
+        for (int r = 1; r < C; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            x[0][h] = make_float4(x[0][h].x + x[r][h].x, x[0][h].y + x[r][h].y,
+                                  x[0][h].z + x[r][h].z, x[0][h].w + x[r][h].w);
+        *reinterpret_cast<uint4*>(a.y + (int64_t)(m0 + row) * a.N + n0 + col) =
+            make_uint4(pack_bf16x2(x[0][0].x, x[0][0].y), pack_bf16x2(x[0][0].z, x[0][0].w),
+                       pack_bf16x2(x[0][1].x, x[0][1].y), pack_bf16x2(x[0][1].z, x[0][1].w));
+      }
+    };
+    if (BN == 64 || split == 1)
+      finish(std::integral_constant<int, 2>{});
+    else
+      finish(std::integral_constant<int, 4>{});
+    __syncwarp();
+    splitk::cluster_sync_all();  // nobody leaves while its sums are read
+  }
+
   // After an abort: wait (bounded) for the loads and MMAs still in flight.
   __syncthreads();
   if (*abort_flag) {
@@ -673,13 +764,20 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, cons
   MxArgs a = a0;
   a.tiles = a.mt * ((a.N + BN - 1) / BN);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  cfg.numAttrs = kDirect ? 0 : 1;  // (the scale pass is what it may overlap)
+  if (!kDirect) {  // (the scale pass is what it may overlap)
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (a.split > 0) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = 1u << a.split;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
   cfg.stream = st;
-  cfg.gridDim = dim3((unsigned)std::min(a.tiles, num_sms()), 1, 1);
+  cfg.gridDim = dim3((unsigned)(a.split > 0 ? a.tiles << a.split : std::min(a.tiles, num_sms())), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = Cfg::kSmem;
   if (cudaLaunchKernelEx(&cfg, mx_gemm_kernel<BN, PL, kDirect>, tx, tw, ty, a, wait_ctl()) != cudaSuccess)
@@ -690,14 +788,15 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, cons
 template <int BN, int PL>
 wq_status launch_width(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a,
                        const ScaleArgs& sa, cudaStream_t st) {
-  // Few rows of scales a stage, and a tile a CTA: the product takes them as they are
-  // and the pass is saved. Two planes, K = 4096, with the pass and without: 33 tokens
-  // x 4096 features 9.8 and 9.2 us, 64 9.5 and 9.5, 96 9.6 and 10.5, 33 x 14336 11.6
-  // and 11.2, 64 11.7 and 12.6; one plane: 33 x 4096 8.7 and 7.3, 128 8.9 and 8.3, 128 x
-  // 14336 10.4 and 11.3.
+  // Few rows of scales, and a tile a CTA: the product takes them as they are and the
+  // pass is saved. Two planes, K = 4096, with the pass and without, K not split: 33
+  // tokens x 4096 features 9.8 and 9.2 us, 64 9.5 and 9.5, 96 9.6 and 10.5, 64 x 14336
+  // 11.7 and 12.6; one plane: 33 x 4096 8.7 and 7.3, 128 8.9 and 8.3, 128 x 14336 10.4
+  // and 11.3. A CTA with few stages may have more rows for the same saving.
   if constexpr (BN <= 128) {
     const int64_t tiles = (int64_t)a.mt * ((a.N + BN - 1) / BN);
-    if (tiles <= num_sms() && PL * std::min(a.M, kBM) + BN <= 176)
+    const int rows = PL * std::min(a.M, kBM) + BN;
+    if (tiles <= num_sms() && (rows <= 176 || rows * (sa.kt >> a.split) <= 2300))
       return launch_gemm_t<BN, PL, true>(tx, wcodes, y, a, st);
   }
   const int64_t blocks = (int64_t)PL * a.mt + (a.N + 127) / 128;
@@ -706,20 +805,44 @@ wq_status launch_width(const CUtensorMap& tx, const void* wcodes, void* y, const
 }
 
 template <int PL>
-wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a,
+wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const MxArgs& a0,
                       const ScaleArgs& sa, cudaStream_t st) {
-  // the tile width with the least time for the slowest CTA: whole tiles an SM
-  // takes, times a tile's cost
-  const int64_t mt = a.mt, sms = num_sms();
-  auto cost = [&](int bn, int64_t tile) {
-    const int64_t tiles = mt * ((a.N + bn - 1) / bn);
-    return (tiles + sms - 1) / sms * tile;
-  };
-  const int64_t c32 = cost(32, 70), c64 = cost(64, 90), c128 = cost(128, 140), c256 = cost(256, 256);
-  if (c256 <= std::min({c128, c64, c32})) return launch_width<256, PL>(tx, wcodes, y, a, sa, st);
-  if (c128 <= std::min(c64, c32)) return launch_width<128, PL>(tx, wcodes, y, a, sa, st);
-  if (c64 <= c32) return launch_width<64, PL>(tx, wcodes, y, a, sa, st);
-  return launch_width<32, PL>(tx, wcodes, y, a, sa, st);
+  // The tile width with the least time for the slowest CTA: whole tiles an SM takes,
+  // times a tile's cost.
+  const int64_t mt = a0.mt, sms = num_sms();
+  auto tiles = [&](int bn) { return mt * (((int64_t)a0.N + bn - 1) / bn); };
+  int bn = 32, split = 0;
+  int64_t least = INT64_MAX;
+  for (auto [width, tile] : {std::pair(256, 256), {128, 140}, {64, 90}, {32, 70}}) {
+    const int64_t cost = (tiles(width) + sms - 1) / sms * tile;
+    if (cost < least) least = cost, bn = width;
+  }
+  // A tile a CTA: its stages, one after the other, are the time (ns a stage; the product
+  // of 33 x 4096 x 11008, two planes, took 18.1 us). Wider tiles whose K is shared by
+  // the CTAs of a cluster have fewer, for the sums' way through shared memory (two
+  // cluster barriers, and BN floats a row): 128 wide and 4 CTAs 11.0 us, 64 and 2 13.3.
+  // With 128 rows and K = 4096 it does not pay: 9.9 us with 32 wide tiles, 12.5 with
+  // 128 and 4; with K = 14336 it does: 23.4 and 15.7.
+  if (tiles(bn) <= sms) {
+    auto time = [&](int width, int s) {
+      const int64_t stage = PL == 1 ? (width == 32 ? 280 : width == 64 ? 330 : 320)
+                                    : (width == 32 ? 340 : width == 64 ? 370 : 390);
+      const int64_t sums = s > 0 ? 1200 + width * std::min(a0.M, kBM) / 4 : 0;
+      return ((sa.kt + (1 << s) - 1) >> s) * stage + sums;
+    };
+    int64_t best = bn <= 128 ? time(bn, 0) : 0;
+    for (auto [width, s] : {std::pair(64, 1), {128, 1}, {128, 2}})
+      if (2 << s <= sa.kt && tiles(width) << s <= 128 && time(width, s) < best)
+        best = time(width, s), bn = width, split = s;
+  }
+  MxArgs a = a0;
+  a.split = split;
+  switch (bn) {
+    case 32: return launch_width<32, PL>(tx, wcodes, y, a, sa, st);
+    case 64: return launch_width<64, PL>(tx, wcodes, y, a, sa, st);
+    case 128: return launch_width<128, PL>(tx, wcodes, y, a, sa, st);
+    default: return launch_width<256, PL>(tx, wcodes, y, a, sa, st);
+  }
 }
 
 template <typename T>
@@ -777,6 +900,7 @@ wq_status launch_mx_gemm(const uint8_t* xc, const uint8_t* xs, int64_t M, int64_
   a.sf = sa.out;
   a.xs = xs;
   a.ws = ws;
+  a.y = static_cast<uint16_t*>(y);
   a.M = (int)M;
   a.N = (int)N;
   a.K = (int)K;

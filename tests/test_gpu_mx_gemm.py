@@ -135,6 +135,18 @@ EDGES = [(20, 4736, 1152), (20, 4752, 1152), (72, 1040, 2176), (73, 1040, 2176),
          (144, 2048, 640), (160, 80, 4224)]
 
 
+# Few tiles and a long K: two and four CTAs share it, its stages dividing and not,
+# rows and features cut inside a tile, one and several row tiles.
+SHARED = [(1, 4096, 4096), (33, 4080, 4224), (5, 1040, 8192), (128, 1024, 8320), (130, 2048, 8192),
+          (400, 1040, 11008), (64, 2000, 2176)]
+
+
+@pytest.mark.parametrize("planes", [1, 2])
+@pytest.mark.parametrize("m,n,k", SHARED)
+def test_product_whose_k_is_shared(wq, m, n, k, planes):
+    test_product(wq, m, n, k, planes)
+
+
 @pytest.mark.parametrize("planes", [1, 2])
 @pytest.mark.parametrize("m,n,k", EDGES)
 def test_product_with_and_without_the_scale_pass(wq, m, n, k, planes):
@@ -226,7 +238,7 @@ def test_empty_and_refusals(wq):
         wq.wq_mx_gemm(p3, s3, 32, codes[:, :48].contiguous(), scales[:, :3].contiguous())
 
 
-@pytest.mark.parametrize("m,n,k", [(200, 512, 1024), (20, 512, 4352)])
+@pytest.mark.parametrize("m,n,k", [(200, 512, 1024), (20, 512, 1152), (20, 2048, 8192)])
 def test_bounded_wait_expires_cleanly(wq, m, n, k):
     """With the loader's first k-tile withheld the kernel gives up, reports the
     wait and returns; the next call is right."""
