@@ -48,6 +48,33 @@ inline wq_status launch_status() {
   return e == cudaSuccess ? WQ_OK : WQ_ERR_CUDA;
 }
 
+// Programmatic dependent launch: the kernel may be set up while the one before it
+// in the stream still runs, and begins with follow_previous() (or a wait of its own).
+// A kernel of a few microseconds saves about one in a chain of such.
+template <typename... K, typename... A>
+inline wq_status launch_following(void (*kernel)(K...), unsigned grid, unsigned block, size_t smem,
+                                  cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...) == cudaSuccess ? launch_status()
+                                                                                 : WQ_ERR_CUDA;
+}
+
+// Everything before this kernel in the stream is complete and visible; then the
+// next kernel may be set up.
+__device__ __forceinline__ void follow_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 inline int num_sms() {
   static int sms = [] {
     int dev = 0, n = 148;

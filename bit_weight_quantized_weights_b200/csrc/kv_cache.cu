@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 16)
                      uint32_t* __restrict__ kc, __half* __restrict__ ks, __half* __restrict__ kz,
                      uint32_t* __restrict__ vc, __half* __restrict__ vs,
                      __half* __restrict__ vz) {
+  follow_previous();
   const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
   const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // units * H < 2^31 - 8
   if (item >= (uint32_t)(p.units * p.H)) return;
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 20)
                    const __half* __restrict__ kz, const uint32_t* __restrict__ vc,
                    const __half* __restrict__ vs, const __half* __restrict__ vz,
                    T* __restrict__ k, T* __restrict__ v) {
+  follow_previous();
   const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
   const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // units * H < 2^31 - 8
   if (item >= (uint32_t)(p.units * p.H)) return;
@@ -458,22 +460,23 @@ KvRows make_rows(int64_t T, int64_t Hkv, const int64_t* k_strides, const int64_t
 }
 
 template <typename T>
-void append(const KvRows& p, const void* k, const void* v, void* const* c, cudaStream_t st) {
+wq_status append(const KvRows& p, const void* k, const void* v, void* const* c, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.units * p.H + kWarps - 1) / kWarps);
-  kv_append_kernel<T><<<grid, 32 * kWarps, 0, st>>>(
-      p, static_cast<const T*>(k), static_cast<const T*>(v), static_cast<uint32_t*>(c[0]),
-      static_cast<__half*>(c[1]), static_cast<__half*>(c[2]), static_cast<uint32_t*>(c[3]),
-      static_cast<__half*>(c[4]), static_cast<__half*>(c[5]));
+  return launch_following(
+      kv_append_kernel<T>, grid, 32 * kWarps, 0, st, p, static_cast<const T*>(k),
+      static_cast<const T*>(v), static_cast<uint32_t*>(c[0]), static_cast<__half*>(c[1]),
+      static_cast<__half*>(c[2]), static_cast<uint32_t*>(c[3]), static_cast<__half*>(c[4]),
+      static_cast<__half*>(c[5]));
 }
 
 template <typename T>
-void read_back(const KvRows& p, void* k, void* v, const void* const* c, cudaStream_t st) {
+wq_status read_back(const KvRows& p, void* k, void* v, const void* const* c, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.units * p.H + kWarps - 1) / kWarps);
-  kv_read_kernel<T><<<grid, 32 * kWarps, 0, st>>>(
-      p, static_cast<const uint32_t*>(c[0]), static_cast<const __half*>(c[1]),
-      static_cast<const __half*>(c[2]), static_cast<const uint32_t*>(c[3]),
-      static_cast<const __half*>(c[4]), static_cast<const __half*>(c[5]), static_cast<T*>(k),
-      static_cast<T*>(v));
+  return launch_following(
+      kv_read_kernel<T>, grid, 32 * kWarps, 0, st, p, static_cast<const uint32_t*>(c[0]),
+      static_cast<const __half*>(c[1]), static_cast<const __half*>(c[2]),
+      static_cast<const uint32_t*>(c[3]), static_cast<const __half*>(c[4]),
+      static_cast<const __half*>(c[5]), static_cast<T*>(k), static_cast<T*>(v));
 }
 
 }  // namespace
@@ -483,13 +486,9 @@ wq_status launch_kv_append(const void* k, const void* v, wq_dtype dt, int64_t T,
                            const int32_t* starts, const int32_t* offsets, int64_t cap,
                            void* const* cache, cudaStream_t st) {
   const KvRows p = make_rows(T, Hkv, k_strides, v_strides, B, starts, offsets, cap);
-  if (dt == WQ_BF16)
-    append<__nv_bfloat16>(p, k, v, cache, st);
-  else if (dt == WQ_FP16)
-    append<__half>(p, k, v, cache, st);
-  else
-    append<float>(p, k, v, cache, st);
-  return launch_status();
+  if (dt == WQ_BF16) return append<__nv_bfloat16>(p, k, v, cache, st);
+  if (dt == WQ_FP16) return append<__half>(p, k, v, cache, st);
+  return append<float>(p, k, v, cache, st);
 }
 
 wq_status launch_kv_read(void* k, void* v, wq_dtype dt, int64_t T, int64_t Hkv,
@@ -497,13 +496,9 @@ wq_status launch_kv_read(void* k, void* v, wq_dtype dt, int64_t T, int64_t Hkv,
                          const int32_t* starts, const int32_t* offsets, int64_t cap,
                          const void* const* cache, cudaStream_t st) {
   const KvRows p = make_rows(T, Hkv, k_strides, v_strides, B, starts, offsets, cap);
-  if (dt == WQ_BF16)
-    read_back<__nv_bfloat16>(p, k, v, cache, st);
-  else if (dt == WQ_FP16)
-    read_back<__half>(p, k, v, cache, st);
-  else
-    read_back<float>(p, k, v, cache, st);
-  return launch_status();
+  if (dt == WQ_BF16) return read_back<__nv_bfloat16>(p, k, v, cache, st);
+  if (dt == WQ_FP16) return read_back<__half>(p, k, v, cache, st);
+  return read_back<float>(p, k, v, cache, st);
 }
 
 }  // namespace wq

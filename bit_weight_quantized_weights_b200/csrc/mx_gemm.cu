@@ -124,6 +124,7 @@ template <typename T, int PL>
 __global__ void __launch_bounds__(256)
     mx_planes_kernel(const T* __restrict__ x, int64_t ldx, int M, int K,
                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  follow_previous();
   const int lane = threadIdx.x & 31;
   const uint32_t chunks = (uint32_t)(K + 511) / 512;
   const uint32_t total = (uint32_t)M * chunks;  // below 2^31
@@ -193,7 +194,7 @@ struct ScaleArgs {
 
 __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
   __shared__ __align__(16) uint32_t sm[8][128];  // piece, then word (r % 32) * 4 + r / 32
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  follow_previous();  // (the product reads codes as soon as it starts)
   const int chunk = blockIdx.x % a.chunks, block = blockIdx.x / a.chunks;
   const int words = a.K / 128;  // 4-byte groups of a row
   const bool is_x = block < a.P * a.xblocks;
@@ -366,6 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm100::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_sf = tmem + Cfg::kAccCols;
+  // With the scale pass before it, this kernel starts when everything older is
+  // complete (and a next call's pass set up early took 1 to 2 us from it).
+  if (kDirect) follow_previous();
 
   int last_issued = -1;
   if (warp == 0) {
@@ -766,10 +770,9 @@ wq_status launch_gemm_t(const CUtensorMap& tx, const void* wcodes, void* y, cons
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
-  if (!kDirect) {  // (the scale pass is what it may overlap)
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   if (a.split > 0) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs].val.clusterDim.x = 1u << a.split;
@@ -800,8 +803,9 @@ wq_status launch_width(const CUtensorMap& tx, const void* wcodes, void* y, const
       return launch_gemm_t<BN, PL, true>(tx, wcodes, y, a, st);
   }
   const int64_t blocks = (int64_t)PL * a.mt + (a.N + 127) / 128;
-  mx_scales_kernel<<<(unsigned)(blocks * sa.chunks), 256, 0, st>>>(sa);
-  return launch_gemm_t<BN, PL, false>(tx, wcodes, y, a, st);
+  wq_status s =
+      launch_following(mx_scales_kernel, (unsigned)(blocks * sa.chunks), 256, 0, st, sa);
+  return s != WQ_OK ? s : launch_gemm_t<BN, PL, false>(tx, wcodes, y, a, st);
 }
 
 template <int PL>
@@ -846,14 +850,12 @@ wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const 
 }
 
 template <typename T>
-void planes(const void* x, int64_t ldx, int M, int K, int P, uint8_t* codes, uint8_t* scales,
+wq_status planes(const void* x, int64_t ldx, int M, int K, int P, uint8_t* codes, uint8_t* scales,
             cudaStream_t st) {
   const int64_t total = (int64_t)M * ((K + 511) / 512);
   const unsigned grid = (unsigned)std::min<int64_t>((total + 7) / 8, (int64_t)num_sms() * 64);
-  if (P == 1)
-    mx_planes_kernel<T, 1><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, M, K, codes, scales);
-  else
-    mx_planes_kernel<T, 2><<<grid, 256, 0, st>>>(static_cast<const T*>(x), ldx, M, K, codes, scales);
+  return launch_following(P == 1 ? mx_planes_kernel<T, 1> : mx_planes_kernel<T, 2>, grid, 256, 0,
+                          st, static_cast<const T*>(x), ldx, M, K, codes, scales);
 }
 
 }  // namespace
@@ -861,12 +863,9 @@ void planes(const void* x, int64_t ldx, int M, int K, int P, uint8_t* codes, uin
 wq_status launch_mx_planes(const void* x, wq_dtype dt, int64_t ldx, int64_t M, int64_t K, int32_t P,
                            uint8_t* codes, uint8_t* scales, cudaStream_t st) {
   if (dt == WQ_BF16)
-    planes<__nv_bfloat16>(x, ldx, (int)M, (int)K, P, codes, scales, st);
-  else if (dt == WQ_FP16)
-    planes<__half>(x, ldx, (int)M, (int)K, P, codes, scales, st);
-  else
-    planes<float>(x, ldx, (int)M, (int)K, P, codes, scales, st);
-  return launch_status();
+    return planes<__nv_bfloat16>(x, ldx, (int)M, (int)K, P, codes, scales, st);
+  if (dt == WQ_FP16) return planes<__half>(x, ldx, (int)M, (int)K, P, codes, scales, st);
+  return planes<float>(x, ldx, (int)M, (int)K, P, codes, scales, st);
 }
 
 // Workspace: the scale pieces of all planes' token blocks and of the weights'

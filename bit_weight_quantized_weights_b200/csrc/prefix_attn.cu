@@ -472,12 +472,16 @@ __device__ __forceinline__ int own_length(const PrefixArgs& p, int b) {
 // rows on 2000 to 2048 own tokens take 43 us (141 MB of cache, issue 51%, HBM 42%).
 // With few keys its latency is what counts: 4 chats on 1021 shared keys 8.6 us with
 // the merge. Launched while the tcgen05 kernel still runs, whose results the merge
-// needs too: every CTA ends by waiting for it.
+// needs too: every CTA ends by waiting for it. Without that kernel it is the call's
+// first and waits at once (ends_waiting false).
 template <int NTP, int NTO>
 __global__ void __launch_bounds__(32 * kWarps, NTP * NTO == 1 ? 4 : 2)
-    prefix_attn_kernel(const __grid_constant__ PrefixArgs p, int nprefix) {
+    prefix_attn_kernel(const __grid_constant__ PrefixArgs p, int nprefix, bool ends_waiting) {
   extern __shared__ __align__(16) uint8_t sm[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (ends_waiting)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  else
+    follow_previous();
   int i = blockIdx.x;
   if (i < nprefix) {
     const int ranges = p.nsp;
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(32 * kWarps, NTP * NTO == 1 ? 4 : 2)
       attend<NTO>(p, p.own, bh * p.own.cap, bh * p.own.nblk, kh, b * p.R, p.R, begin,
                   min(begin + p.chunk_o, len), p.nsp + range, sm);
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (ends_waiting) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // The ranges' partial results of a row against their common bound. W warps a
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   const int64_t base = (int64_t)row * (p.nsp + p.nso);
   const int run = (n + W - 1) / W;
   const int end = min((part + 1) * run, n);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  follow_previous();
   float m = kNone, e = 0.0f;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int j0 = part * run; j0 < end; j0 += 32) {
@@ -674,36 +678,23 @@ Plan make_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t P, int64_t cap) {
 
 template <int NTP, int NTO>
 wq_status launch(const PrefixArgs& a, int tc, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.stream = st;
   if (tc) {
-    wq_status s = launch_prefix_tc(a, tc, st);
+    const wq_status s = launch_prefix_tc(a, tc, st);
     if (s != WQ_OK) return s;
-    cfg.numAttrs = 1;
   }
   const int nprefix = tc ? 0 : a.nprefix;
   constexpr int kSmem = attn_smem<(NTP > NTO ? NTP : NTO)>();
   static std::atomic<uint64_t> smem_set{0};
   if (!allow_smem(prefix_attn_kernel<NTP, NTO>, kSmem, smem_set)) return WQ_ERR_CUDA;
-  cfg.gridDim = dim3((unsigned)(nprefix + (int64_t)a.nso * a.Hkv * a.B), 1, 1);
-  cfg.blockDim = dim3(32 * kWarps, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
-  if (cudaLaunchKernelEx(&cfg, prefix_attn_kernel<NTP, NTO>, a, nprefix) != cudaSuccess)
-    return WQ_ERR_CUDA;
-  cfg.numAttrs = 1;
+  const wq_status s = launch_following(prefix_attn_kernel<NTP, NTO>,
+                                       (unsigned)(nprefix + (int64_t)a.nso * a.Hkv * a.B),
+                                       32 * kWarps, kSmem, st, a, nprefix, tc != 0);
+  if (s != WQ_OK) return s;
   const int64_t rows = (int64_t)a.B * a.Hq;
   const int warps = a.nsp + a.nso <= 12 ? 1 : kMergeWarps;
-  cfg.gridDim = dim3((unsigned)((rows * warps + kMergeWarps - 1) / kMergeWarps), 1, 1);
-  cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
-  cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, warps == 1 ? prefix_merge_kernel<1> : prefix_merge_kernel<kMergeWarps>,
-                         a) != cudaSuccess)
-    return WQ_ERR_CUDA;
-  return launch_status();
+  return launch_following(warps == 1 ? prefix_merge_kernel<1> : prefix_merge_kernel<kMergeWarps>,
+                          (unsigned)((rows * warps + kMergeWarps - 1) / kMergeWarps),
+                          32 * kMergeWarps, 0, st, a);
 }
 
 template <int NTO>

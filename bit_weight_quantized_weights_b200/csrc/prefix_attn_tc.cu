@@ -169,8 +169,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   // this CTA's KV head, row tiles and keys
   const int splits = MT == 2 ? p.nsp : p.nsp / 2;
   const int split = blockIdx.x % splits;
@@ -204,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   sm100::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  follow_previous();  // (the kernel of the own tokens reads as soon as it starts)
 
   auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
     // one suspended poll of up to 20 us covers the waits of a running pipeline
@@ -720,8 +719,8 @@ template <int MT, bool kExact>
 wq_status launch(const PrefixArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> smem_set{0};
   if (!allow_smem(prefix_tc_kernel<MT, kExact>, smem_bytes<MT>(), smem_set)) return WQ_ERR_CUDA;
-  prefix_tc_kernel<MT, kExact><<<(unsigned)a.nprefix, kThreads, smem_bytes<MT>(), st>>>(a, wait_ctl());
-  return launch_status();
+  return launch_following(prefix_tc_kernel<MT, kExact>, (unsigned)a.nprefix, kThreads,
+                          smem_bytes<MT>(), st, a, wait_ctl());
 }
 
 }  // namespace
