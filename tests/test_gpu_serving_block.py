@@ -175,3 +175,49 @@ def test_operators_on_two_streams_at_once(wq):
     assert wq.wq_device_error()[0] == wq.WQ_OK
     for outs in got[0] + got[1]:
         assert all(torch.equal(a, c) for a, c in zip(outs, want))
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_a_chain_without_waits(wq, path):
+    """Every call reads what the call before it wrote, with torch operations
+    between some of them: the same results as with a synchronization after each."""
+    b, hkv, cap, n = 16, 2, 70, 1024
+    g = torch.Generator().manual_seed(5)
+    x0 = torch.randn(b, n, generator=g).bfloat16().cuda()
+    weights = [wq.wq_mx_quantize((torch.randn(n, n, generator=g) * 0.03).cuda()) for _ in range(2)]
+    prompt = [torch.randn(200, hkv, D, generator=g).bfloat16().cuda() for _ in range(2)]
+    i32 = lambda v: torch.tensor(list(v), dtype=torch.int32, device="cuda")
+    edges, zero = i32(range(b + 1)), i32([0])
+
+    def run(wait):
+        pre, own = wq.kv_cache_alloc(1, hkv, 200), wq.kv_cache_alloc(b, hkv, cap)
+        wq.wq_kv_append(*prompt, *pre, zero, i32([0, 200]))
+        x, outs, starts = x0.clone(), [], i32([0] * b)
+        for step in range(40):
+            planes, scales = wq.wq_mx_quantize_planes(x, 2)
+            wait()
+            y = wq.wq_mx_gemm(planes, scales, n, *weights[0])
+            wait()
+            q = y.view(b, 8, D)
+            wq.wq_kv_append(q[:, :2], q[:, 2:4], *own, starts, edges)
+            wait()
+            starts += 1
+            o = wq.wq_prefix_attention(q, *pre, *own, starts)
+            wait()
+            k, v = wq.wq_kv_read(*own, starts - 1, edges, b)
+            planes, scales = wq.wq_mx_quantize_planes(o.view(b, n), 1)
+            wait()
+            x = wq.wq_mx_gemm(planes, scales, n, *weights[1])
+            wait()
+            x = (x + x0).clamp(-4, 4)
+            outs += [y, o, k, v, x]
+        return outs
+
+    wq.wq_test_set_prefix_path(path)
+    try:
+        want = run(torch.cuda.synchronize)
+        for _ in range(3):
+            assert all(torch.equal(a, c) for a, c in zip(run(lambda: None), want))
+    finally:
+        wq.wq_test_set_prefix_path(0)
+    assert wq.wq_device_error()[0] == wq.WQ_OK
