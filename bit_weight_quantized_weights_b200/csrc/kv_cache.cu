@@ -12,7 +12,8 @@
 // (16-bit types) and writes 68 B, the read-back the reverse. The read is bound by
 // HBM (127315 tokens x 8 heads, bf16: 660 MB in 110 us, 91% of a copy's rate), the
 // append by its instructions, about 1000 a warp for 16 rows (12891 tokens x 8
-// heads: 67 MB in 17.3 us, 59% of a copy's rate). The unit of work is one V block, 8 cache positions of one
+// heads: 67 MB in 16.6 us, 61% of a copy's rate). The unit of work is one V block,
+// 8 cache positions of one
 // (sequence, head), taken by one warp: 16 lanes hold a row (8 elements a lane,
 // one 16-byte access), the two halves of the warp hold two rows, four steps
 // cover the block. So a V word has one writer (no atomics; the nibbles of

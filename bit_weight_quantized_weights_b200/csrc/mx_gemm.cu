@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 // a long K, the 2 or 4 CTAs of a cluster share a tile's K. 8192 x 14336 x 4096 with two
 // planes: 325 us with the scale pass, 5.9 POP/s, the tensor cores busy 81% of the
 // cycles (bare MMAs: 6.7 POP/s at the same power); with one plane 197 us, bound by
-// the operands' way from L2; 33 x 4096 x 4096 7.5 us, bound by latency.
+// the operands' way from L2; 33 x 4096 x 4096 7.0 us, bound by latency.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128;
 constexpr int kBKBytes = 128;   // bytes of a stage's row: 256 k

@@ -32,7 +32,7 @@
 // dequantization 3100); a stream's scores, softmax and values follow one another and
 // two streams cover each other in part. 1024 rows x 8 heads x 65537 keys, with the
 // own tokens and the merge: 314 us with bf16 queries (877 TFLOP/s), 425 with fp16;
-// 512 x 8 x 32768: 104 us.
+// 512 x 8 x 32768: 100 us.
 //
 // MMAs of one issuing thread execute in order, so S of a tile completes after
 // the O += P V issued before it: when a softmax warp sees its scores it may
