@@ -68,10 +68,16 @@ inline wq_status launch_following(void (*kernel)(K...), unsigned grid, unsigned 
                                                                                  : WQ_ERR_CUDA;
 }
 
-// Everything before this kernel in the stream is complete and visible; then the
-// next kernel may be set up.
-__device__ __forceinline__ void follow_previous() {
+// Everything before this kernel in the stream is complete and visible.
+__device__ __forceinline__ void wait_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The same; then the next kernel may be set up, while this one writes. Not for a
+// kernel that writes INT4 or NF4 codes, scales or zeros: the decode GEMV loads its
+// weights before it waits (their kernels leave the next one's start to their end).
+__device__ __forceinline__ void follow_previous() {
+  wait_previous();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 

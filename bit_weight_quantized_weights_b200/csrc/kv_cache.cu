@@ -260,7 +260,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 8 : 16)
                      uint32_t* __restrict__ kc, __half* __restrict__ ks, __half* __restrict__ kz,
                      uint32_t* __restrict__ vc, __half* __restrict__ vs,
                      __half* __restrict__ vz) {
-  follow_previous();
+  // no early start of the next kernel: a decode GEMV over the K rows (one head's
+  // codes, scales and zeros are INT4 weights of group 128) reads them at once
+  wait_previous();
   const int lane = threadIdx.x & 31, half = lane >> 4, col = lane & 15;
   const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);  // units * H < 2^31 - 8
   if (item >= (uint32_t)(p.units * p.H)) return;

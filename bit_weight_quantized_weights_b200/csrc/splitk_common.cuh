@@ -430,7 +430,8 @@ wq_status launch_split(Kern kern, const Plan& pl, int threads, int64_t N, cudaSt
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   // early: programmatic dependent launch after the preceding kernel, which
-  // must only read what this kernel reads before its griddepcontrol.wait
+  // must not have started this one (griddepcontrol.launch_dependents) before it
+  // wrote what this kernel reads before its griddepcontrol.wait
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
