@@ -145,6 +145,26 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _scratch(stream, alloc, *args, **kwargs):
+    """Memory for a call on `stream` (None: the current one), from that stream's pool:
+    memory of another pool may still be in use on the stream it belongs to, and what
+    the wrapper drops would go back there while the call runs."""
+    if stream is None:
+        return alloc(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        return alloc(*args, **kwargs)
+
+
+def _result(stream, alloc, *args, **kwargs):
+    """The same for what the caller gets, who will use it on the current stream too."""
+    out = _scratch(stream, alloc, *args, **kwargs)
+    if stream is not None:
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(t.device))
+    return out
+
+
 # The current device and a device's current stream, as integers: a call of a few
 # microseconds on the GPU is launched from here, and the Stream objects of
 # torch.cuda.current_stream() cost as much as the launch.
@@ -213,7 +233,7 @@ def wq_quantize_pack(fmt, w, group, qweight=None, scales=None, zeros=None, strea
     _cuda(w, torch.float32, "W")
     n, k = w.shape
     if qweight is None:
-        qweight, scales, zeros = alloc_packed(fmt, n, k, group, w.device)
+        qweight, scales, zeros = _result(stream, alloc_packed, fmt, n, k, group, w.device)
     _check(lib.wq_quantize_pack(fmt, _ptr(w), n, k, group, _ptr(qweight), _ptr(scales),
                                 _ptr(zeros), _stream(stream)), "wq_quantize_pack")
     return qweight, scales, zeros
@@ -222,7 +242,7 @@ def wq_quantize_pack(fmt, w, group, qweight=None, scales=None, zeros=None, strea
 def wq_unpack(fmt, qweight, n, k, out=None, stream=None):
     _cuda(qweight, None, "qweight")
     if out is None:
-        out = torch.empty(n * k, dtype=torch.uint8, device=qweight.device)
+        out = _result(stream, torch.empty, n * k, dtype=torch.uint8, device=qweight.device)
     _check(lib.wq_unpack(fmt, _ptr(qweight), n, k, _ptr(out), _stream(stream)), "wq_unpack")
     return out
 
@@ -231,7 +251,7 @@ def wq_nf4_dequant(codes, absmax, numel, out=None, out_dtype=torch.bfloat16, str
     _cuda(codes, torch.uint8, "codes")
     _cuda(absmax, torch.float32, "absmax")
     if out is None:
-        out = torch.empty(numel, dtype=out_dtype, device=codes.device)
+        out = _result(stream, torch.empty, numel, dtype=out_dtype, device=codes.device)
     dt = WQ_BF16 if out.dtype == torch.bfloat16 else WQ_FP16
     _check(lib.wq_nf4_dequant(_ptr(codes), _ptr(absmax), numel, 64, _ptr(out), dt,
                               _stream(stream)), "wq_nf4_dequant")
@@ -244,7 +264,7 @@ def wq_int4_dequant(qweight, scales, zeros, n, k, group, out=None, out_dtype=tor
     _cuda(scales, torch.float16, "scales")
     _cuda(zeros, torch.float16, "zeros")
     if out is None:
-        out = torch.empty(n, k, dtype=out_dtype, device=qweight.device)
+        out = _result(stream, torch.empty, n, k, dtype=out_dtype, device=qweight.device)
     dt = WQ_BF16 if out.dtype == torch.bfloat16 else WQ_FP16
     _check(lib.wq_int4_dequant(_ptr(qweight), _ptr(scales), _ptr(zeros), n, k, group, _ptr(out),
                                dt, _stream(stream)), "wq_int4_dequant")
@@ -255,7 +275,7 @@ def _product(fn, name, x, n, fmt, group, qweight, scales, zeros, out, workspace,
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _cuda(out, torch.bfloat16, "y")
     ws = _ptr(workspace)
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -275,7 +295,7 @@ def wq_residual(fmt, w, group, qweight, scales, zeros, out=None, stream=None):
     _cuda(w, torch.float32, "W")
     n, k = w.shape
     if out is None:
-        out = torch.empty(k, n, dtype=torch.float16, device=w.device)
+        out = _result(stream, torch.empty, k, n, dtype=torch.float16, device=w.device)
     _cuda(out, torch.float16, "residual_t")
     _check(lib.wq_residual(fmt, _ptr(w), n, k, group, _ptr(qweight), _ptr(scales), _ptr(zeros),
                            _ptr(out), _stream(stream)), "wq_residual")
@@ -287,7 +307,7 @@ def wq_select_salient(x, k, out=None, stream=None):
     _cuda(x, torch.bfloat16, "x")
     m, kk = x.shape
     if out is None:
-        out = torch.empty(max(k, 0), dtype=torch.int32, device=x.device)
+        out = _result(stream, torch.empty, max(k, 0), dtype=torch.int32, device=x.device)
     _cuda(out, torch.int32, "idx")
     _check(lib.wq_select_salient(_ptr(x), m, kk, k, _ptr(out), _stream(stream)),
            "wq_select_salient")
@@ -300,7 +320,7 @@ def wq_w4a16_gemv_corrected(x, n, fmt, group, qweight, scales, zeros, residual_t
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _cuda(out, torch.bfloat16, "y")
     nsel = 0 if idx is None else idx.numel()
     _check(lib.wq_w4a16_gemv_corrected(_ptr(x), m, n, k, fmt, group, _ptr(qweight), _ptr(scales),
@@ -317,10 +337,10 @@ def wq_w4a16_gemv_salient(x, n, fmt, group, qweight, scales, zeros, residual_t, 
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _cuda(out, torch.bfloat16, "y")
     if idx is None:
-        idx = torch.empty(max(nsel, 1), dtype=torch.int32, device=x.device)
+        idx = _scratch(stream, torch.empty, max(nsel, 1), dtype=torch.int32, device=x.device)
     _cuda(idx, torch.int32, "idx")
     _check(lib.wq_w4a16_gemv_salient(_ptr(x), m, n, k, fmt, group, _ptr(qweight), _ptr(scales),
                                      _ptr(zeros), _ptr(residual_t), nsel, _ptr(idx), _ptr(out),
@@ -338,7 +358,7 @@ def wq_w4a16_gemm(x, n, fmt, group, qweight, scales, zeros, workspace=None, out=
     """Prefill GEMM with fused dequantization on tcgen05: y bf16 [M, N]."""
     _cuda(x, torch.bfloat16, "x")
     if workspace is None:
-        workspace = gemm_workspace(x.shape[0], n, x.shape[1], group, x.device)
+        workspace = _scratch(stream, gemm_workspace, x.shape[0], n, x.shape[1], group, x.device)
     return _product(lib.wq_w4a16_gemm, "wq_w4a16_gemm", x, n, fmt, group, qweight, scales, zeros,
                     out, workspace, stream)
 
@@ -348,8 +368,9 @@ def wq_msd_decompose(x, n_components=2, digits=None, comp_scales=None, stream=No
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if digits is None:
-        digits = torch.empty(n_components, m, k, dtype=torch.int8, device=x.device)
-        comp_scales = torch.empty(n_components, m, dtype=torch.float32, device=x.device)
+        digits = _result(stream, torch.empty, n_components, m, k, dtype=torch.int8, device=x.device)
+        comp_scales = _result(stream, torch.empty, n_components, m, dtype=torch.float32,
+                              device=x.device)
     _check(lib.wq_msd_decompose(_ptr(x), m, k, n_components, _ptr(digits), _ptr(comp_scales),
                                 _stream(stream)), "wq_msd_decompose")
     return digits, comp_scales
@@ -366,9 +387,9 @@ def wq_msd_gemm(x, n, n_components, group, qweight, scales, zeros, workspace=Non
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if workspace is None:
-        workspace = msd_workspace(m, n, k, group, n_components, x.device)
+        workspace = _scratch(stream, msd_workspace, m, n, k, group, n_components, x.device)
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_msd_gemm(_ptr(x), m, n, k, n_components, group, _ptr(qweight), _ptr(scales),
                            _ptr(zeros), _ptr(out), _ptr(workspace),
                            workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -384,7 +405,7 @@ def wq_msd_gemm_noalloc(x, n, n_components, group, qweight, scales, zeros, out=N
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_msd_gemm_noalloc(_ptr(x), m, n, k, n_components, group, _ptr(qweight),
                                    _ptr(scales), _ptr(zeros), _ptr(out), _stream(stream)),
            "wq_msd_gemm_noalloc")
@@ -410,9 +431,9 @@ def wq_mx_quantize(w, codes=None, scales=None, stream=None):
     _cuda(w, torch.float32, "w")
     n, k = w.shape
     if codes is None:
-        codes = torch.empty(n, k // 2, dtype=torch.uint8, device=w.device)
+        codes = _result(stream, torch.empty, n, k // 2, dtype=torch.uint8, device=w.device)
     if scales is None:
-        scales = torch.empty(n, k // 32, dtype=torch.uint8, device=w.device)
+        scales = _result(stream, torch.empty, n, k // 32, dtype=torch.uint8, device=w.device)
     _check(lib.wq_mx_quantize(_ptr(w), n, k, _ptr(codes), _ptr(scales), _stream(stream)),
            "wq_mx_quantize")
     return codes, scales
@@ -423,9 +444,10 @@ def wq_mx_decompose(x, n_passes=2, planes=None, scales=None, stream=None):
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if planes is None:
-        planes = torch.empty(n_passes, m, k, dtype=torch.uint8, device=x.device)
+        planes = _result(stream, torch.empty, n_passes, m, k, dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = torch.empty(n_passes, m, k // 32, dtype=torch.uint8, device=x.device)
+        scales = _result(stream, torch.empty, n_passes, m, k // 32, dtype=torch.uint8,
+                         device=x.device)
     _check(lib.wq_mx_decompose(_ptr(x), m, k, n_passes, _ptr(planes), _ptr(scales),
                                _stream(stream)), "wq_mx_decompose")
     return planes, scales
@@ -441,9 +463,9 @@ def wq_mx_gemv(x, n, n_passes, codes, scales, workspace=None, out=None, stream=N
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if workspace is None:
-        workspace = mx_workspace(m, n, k, n_passes, x.device)
+        workspace = _scratch(stream, mx_workspace, m, n, k, n_passes, x.device)
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_mx_gemv(_ptr(x), m, n, k, n_passes, _ptr(codes), _ptr(scales), _ptr(out),
                           _ptr(workspace), workspace.numel(), _stream(stream)), "wq_mx_gemv")
     return out
@@ -461,12 +483,12 @@ def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     if inner != 1 and k > 1:
         raise ValueError("the rows of x must be contiguous")
     if planes is None:
-        planes = x.new_empty((n_planes, m, k // 2), dtype=torch.uint8)
+        planes = _result(stream, x.new_empty, (n_planes, m, k // 2), dtype=torch.uint8)
     elif planes.dtype is not torch.uint8 or planes.shape != (n_planes, m, k // 2) or \
             not planes.is_contiguous():
         raise ValueError("planes must be uint8 [%d, %d, %d]" % (n_planes, m, k // 2))
     if scales is None:
-        scales = planes.new_empty((n_planes, m, k // 32))
+        scales = _result(stream, planes.new_empty, (n_planes, m, k // 32))
     elif scales.dtype is not torch.uint8 or scales.shape != (n_planes, m, k // 32) or \
             not scales.is_contiguous():
         raise ValueError("scales must be uint8 [%d, %d, %d]" % (n_planes, m, k // 32))
@@ -504,9 +526,9 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
         raise ValueError("scales or weights do not match planes %s and N = %d"
                          % (tuple(planes.shape), n))
     if workspace is None:
-        workspace = mx_gemm_workspace(m, n, k, p, planes.device)
+        workspace = _scratch(stream, mx_gemm_workspace, m, n, k, p, planes.device)
     if out is None:
-        out = planes.new_empty((m, n), dtype=torch.bfloat16)
+        out = _result(stream, planes.new_empty, (m, n), dtype=torch.bfloat16)
     elif out.dtype is not torch.bfloat16 or out.shape != (m, n) or not out.is_contiguous():
         raise ValueError("y must be bfloat16 [%d, %d], contiguous" % (m, n))
     if planes.get_device() != dev or plane_scales.get_device() != dev or \
@@ -527,9 +549,9 @@ def wq_msd_gemm_nf4(x, n, n_components, codes, absmax, workspace=None, out=None,
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if workspace is None:
-        workspace = msd_workspace(m, n, k, 64, n_components, x.device)
+        workspace = _scratch(stream, msd_workspace, m, n, k, 64, n_components, x.device)
     if out is None:
-        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
+        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_msd_gemm_nf4(_ptr(x), m, n, k, n_components, _ptr(codes), _ptr(absmax),
                                _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "wq_msd_gemm_nf4")
@@ -552,7 +574,7 @@ def wq_kv_block_values(codes, rows, length, d, out=None, stream=None):
     _cuda(codes, torch.int32, "codes")
     nblk = (length + 7) // 8
     if out is None:
-        out = torch.empty(rows, nblk, d, dtype=torch.int32, device=codes.device)
+        out = _result(stream, torch.empty, rows, nblk, d, dtype=torch.int32, device=codes.device)
     _check(lib.wq_kv_block_values(_ptr(codes), rows, length, d, _ptr(out), _stream(stream)),
            "wq_kv_block_values")
     return out
@@ -675,10 +697,10 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
     dev = _current_device()
     b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     if k_out is None:
-        k_out = k_cache[1].new_empty((total, hkv, d), dtype=dtype)
+        k_out = _result(stream, k_cache[1].new_empty, (total, hkv, d), dtype=dtype)
     if v_out is None:
-        v_out = torch.empty_like(k_out) if k_out.is_contiguous() else \
-            k_out.new_empty((total, hkv, d))
+        v_out = _result(stream, torch.empty_like, k_out) if k_out.is_contiguous() else \
+            _result(stream, k_out.new_empty, (total, hkv, d))
     t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets, dev)
     if t != total:
         raise ValueError("k_out and v_out must have %d rows" % total)
@@ -738,9 +760,11 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
         pre = (kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(),
                vscale.data_ptr(), vzero.data_ptr())
     if workspace is None:
-        workspace = prefix_attention_workspace(b, hq, hkv, prefix_len, cap, d, q.device)
+        workspace = _scratch(stream, prefix_attention_workspace, b, hq, hkv, prefix_len, cap, d,
+                             q.device)
     if out is None:
-        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
+        out = _result(stream, torch.empty_like, q) if q.is_contiguous() else \
+            _result(stream, q.new_empty, shape)
     elif out.dtype is not kind or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must have q's type and shape, contiguous")
     if q.get_device() != dev or lengths.get_device() != dev or \
@@ -787,9 +811,10 @@ def wq_msd_decode_attention(q, k_cache, v_cache, n_components=2, workspace=None,
             tuple(vz.shape) != tuple(ks.shape) or ks.shape[0] != b:
         raise ValueError("KV cache shapes do not match q")
     if workspace is None:
-        workspace = attention_workspace(b, hq, hkv, length, d, n_components, q.device)
+        workspace = _scratch(stream, attention_workspace, b, hq, hkv, length, d, n_components,
+                             q.device)
     if out is None:
-        out = torch.empty(b, hq, d, dtype=torch.bfloat16, device=q.device)
+        out = _result(stream, torch.empty, b, hq, d, dtype=torch.bfloat16, device=q.device)
     _check(lib.wq_msd_decode_attention(_ptr(q), b, hq, hkv, length, d, n_components, _ptr(kq),
                                        _ptr(ks), _ptr(kz), _ptr(vq), _ptr(vs), _ptr(vz), _ptr(out),
                                        _ptr(workspace), workspace.numel(), _stream(stream)),
