@@ -240,7 +240,8 @@ __device__ __forceinline__ int code_of(float a, float s, float y, int z) {
       15);
 }
 
-// Scale, its reciprocal and the zero of a row's range.
+// Scale, its reciprocal and the zero of a row's range. A row of an infinite scale is
+// coded with the reciprocal 0 (of s = 1, so that div_by's residual is finite).
 __device__ __forceinline__ void row_scale(float lo, float hi, __half& sh, float& s, float& y,
                                           int& z) {
   // (hi - lo) / 15 rounded to nearest
@@ -252,6 +253,12 @@ __device__ __forceinline__ void row_scale(float lo, float hi, __half& sh, float&
   s = __half2float(sh);
   y = __frcp_rn(s);
   z = code_of(div_by(-lo, s, y), 0);
+  if (!(s <= 65504.0f)) {  // beyond fp16 (or hi - lo beyond fp32): x / s is 0 for every x
+    sh = __ushort_as_half((unsigned short)0x7C00u);
+    s = 1.0f;
+    y = 0.0f;
+    z = 0;
+  }
 }
 
 template <typename T>

@@ -1,0 +1,52 @@
+"""INT4 cache rows at the ends of the types' ranges, bit for bit against the oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kvcache
+from tests.test_gpu_kvcache import DTYPES, Pair, _i32
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+
+
+@pytest.fixture(scope="module")
+def wq():
+    from bit_weight_quantized_weights_b200 import binding
+    return binding
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_whose_scale_is_infinite(wq, dtype):
+    """Finite rows with (max - min) / 15 beyond fp16, or max - min beyond fp32: scale
+    infinite, zero point and codes 0, as the quantizer of the weights has it; the rows
+    between them and their V words are not touched by it."""
+    g = torch.Generator().manual_seed(12)
+    x = torch.randn(11, 1, D, generator=g)
+    x[0, 0, 3], x[0, 0, 90] = -491400.0, 491400.0        # 982800 / 15 = 65520: rounds up
+    x[2, 0, 0] = 1e6
+    x[3, 0, 127] = -1e6
+    x[5] = torch.randn(D, generator=g) * 1e7
+    x[6, 0, 8], x[6, 0, 9] = 3e38, -3e38
+    x[7] = 3e38
+    x[8] = -3.3e38
+    x[10, 0, 1] = 982000.0                               # the largest scale: 65472 rounds to it
+    rows = x.to(DTYPES[dtype]).cuda()
+    c = Pair(wq, 1, 1, 16, 9)
+    with np.errstate(all="ignore"):
+        c.append(wq, rows, rows, [3], [0, 11])
+    assert np.isinf(c.host[0][1]).sum() >= 6
+    c.check()
+    codes, scales, zeros = wq.wq_quantize_pack(wq.WQ_FMT_INT4_ASYM,
+                                               rows.float().view(11, D).contiguous(), D)
+    for got, want in zip(c.k, (codes, scales[:, 0], zeros[:, 0])):
+        assert torch.equal(got[0, 0, 3:14], want)
+    for out in DTYPES.values():
+        with np.errstate(all="ignore"):
+            for got, cache in zip(wq.wq_kv_read(c.k, c.v, _i32([3]), _i32([0, 11]), 11, dtype=out),
+                                  c.host):
+                want = torch.from_numpy(kvcache.read(cache, [3], [0, 11], 11)).to(out)
+                assert torch.equal(got.cpu().isnan(), want.isnan())
+                assert torch.equal(got.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
