@@ -31,8 +31,8 @@
 // and its exponentials 2050 each, its 11200 warp instructions 2800 (softmax 5600,
 // dequantization 3100); a stream's scores, softmax and values follow one another and
 // two streams cover each other in part. 1024 rows x 8 heads x 65537 keys, with the
-// own tokens and the merge: 314 us with bf16 queries (877 TFLOP/s), 425 with fp16;
-// 512 x 8 x 32768: 100 us.
+// own tokens and the merge: 306 us with bf16 queries (898 TFLOP/s), 392 with fp16;
+// 512 x 8 x 32768: 98 and 118 us.
 //
 // MMAs of one issuing thread execute in order, so S of a tile completes after
 // the O += P V issued before it: when a softmax warp sees its scores it may
@@ -387,9 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
               sum = fmaxf(sum, __shfl_xor_sync(0xffffffffu, sum, o));
             }
-            // a row moves by its own scores only; t is relative to the old bound
-            const float up = first || sum > kSumMax ? mx : 0.0f;
-            f[n] = first ? 1.0f : ex2(-up);
+            // a row moves by its own scores only; t is relative to the old bound.
+            // Bounds are integers: 2^-up is exact, and so are the products with it
+            const float up = first || sum > kSumMax ? rintf(mx) : 0.0f;
+            f[n] = first ? 1.0f : up < 126.0f ? pow2(-(int)up) : 0.0f;
             m[n] += up;
             E[n] *= f[n];
 #pragma unroll
@@ -417,9 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t o[8];
               tmem_ld_16x128b_x4(ts + 16 * k, o);
               sm100::tmem_ld_wait();
-              const __half2 f0 = __float2half2_rn(f[0]), f1 = __float2half2_rn(f[1]);
+              // (in fp32: 2^-up is below fp16's range from 2^-25 on, a weight times it not yet)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = h2(__hmul2(as_h2(o[j]), (j & 1) ? f1 : f0));
+              for (int j = 0; j < 8; ++j) {
+                const float2 x = __half22float2(as_h2(o[j]));
+                o[j] = pack_f16x2(x.x * f[j & 1], x.y * f[j & 1]);
+              }
               tmem_st_16x128b_x4(ts + 16 * k, o);
             }
           }
