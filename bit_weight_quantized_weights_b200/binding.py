@@ -170,7 +170,7 @@ def _result(stream, alloc, *args, **kwargs):
 # torch.cuda.current_stream() cost as much as the launch.
 _current_device = torch.cuda.current_device
 _BF16, _F16, _I32, _U8 = torch.bfloat16, torch.float16, torch.int32, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # (None without CUDA)
 
 
 def _cuda(t, dtype, name):

@@ -3,8 +3,12 @@ given stream comes from that stream's pool."""
 
 import ast
 import contextlib
+import subprocess
+import sys
 
 import pytest
+
+from tests.conftest import ROOT
 
 
 @pytest.fixture(scope="module")
@@ -67,3 +71,15 @@ def test_no_wrapper_with_a_stream_allocates_past_it(wq):
                 assert not name.startswith(("empty", "zeros", "new_", "alloc_")) and \
                     not name.endswith("workspace"), (fn.name, name, call.lineno)
     assert checked >= 25
+
+
+def test_host_calls_work_on_a_torch_without_cuda(wq):
+    """Sizes, the codebook and refusals need neither a GPU nor torch's CUDA bindings."""
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "from bit_weight_quantized_weights_b200 import binding as wq\n"
+            "assert len(wq.wq_nf4_codebook()) == 16\n"
+            "assert wq.wq_workspace_bytes(wq.WQ_OP_MX_GEMM, 4, 256, 512, 0, 2) > 0\n"
+            "assert wq.lib.wq_kv_append(*[None] * 2, 0, -1, 1, 128, None, None, 1, None, None, 8, "
+            "*[None] * 7) == wq.WQ_ERR_INVALID_ARG\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=300)
