@@ -691,9 +691,10 @@ def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
 def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k_out=None,
                v_out=None, stream=None):
     """Rows of an INT4 cache read back: (k, v) [total, Hkv, D] of dtype bf16,
-    fp16 or fp32, token t of sequence b (offsets[b] <= t < offsets[b + 1]) from
-    cache position starts[b] + t - offsets[b]. Rows behind offsets[B] of a
-    given k_out and v_out stay as they were."""
+    fp16 or fp32 (k_out's and v_out's where they are given), token t of sequence
+    b (offsets[b] <= t < offsets[b + 1]) from cache position starts[b] + t -
+    offsets[b]. Rows behind offsets[B] of a given k_out and v_out stay as they
+    were."""
     dev = _current_device()
     b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     if k_out is None:
@@ -747,6 +748,8 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
     if lengths.dtype is not _I32 or lengths.shape != (b,) or not lengths.is_contiguous():
         raise ValueError("lengths must be int32 [%d], contiguous" % b)
     if prefix_k is None and prefix_v is None:
+        if prefix_len:
+            raise ValueError("prefix_len is %d, but there is no prefix cache" % prefix_len)
         pre = (None,) * 6
         pcap, prefix_len = 0, 0
     else:

@@ -50,3 +50,12 @@ def test_rows_whose_scale_is_infinite(wq, dtype):
                 want = torch.from_numpy(kvcache.read(cache, [3], [0, 11], 11)).to(out)
                 assert torch.equal(got.cpu().isnan(), want.isnan())
                 assert torch.equal(got.cpu().nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+def test_a_prefix_length_without_a_prefix_is_refused(wq):
+    own = wq.kv_cache_alloc(2, 1, 8)
+    q = torch.zeros(2, 4, D, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        wq.wq_prefix_attention(q, None, None, *own, _i32([1, 2]), prefix_len=5)
+    for none in (None, 0):
+        assert not wq.wq_prefix_attention(q, None, None, *own, _i32([0, 0]), prefix_len=none).any()
