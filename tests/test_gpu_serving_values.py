@@ -59,3 +59,24 @@ def test_a_prefix_length_without_a_prefix_is_refused(wq):
         wq.wq_prefix_attention(q, None, None, *own, _i32([1, 2]), prefix_len=5)
     for none in (None, 0):
         assert not wq.wq_prefix_attention(q, None, None, *own, _i32([0, 0]), prefix_len=none).any()
+
+
+def test_offsets_that_decrease_leave_the_rows_around(wq):
+    """Arrays that break the contract: the read-back's rows before and behind both outputs,
+    and the cache's sequences around, keep their values."""
+    h, t, cap = 2, 32, 16
+    k_cache, v_cache = wq.kv_cache_alloc(5, h, cap)
+    inner = [tuple(x[1:4] for x in part) for part in (k_cache, v_cache)]
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(t, h, D, generator=g).bfloat16().cuda() for _ in range(2))
+    for starts, edges in (([0, 3, 9], [5, 2, 40, 7]), ([2 ** 31 - 1, -2 ** 31, 0], [0, 32, 1, 31]),
+                          ([0, 0, 0], [-9, 4, 99, 1000]), ([-7, 4, 15], [32, 31, 30, -1])):
+        wq.wq_kv_append(k, v, *inner, _i32(starts), _i32(edges))
+        for dtype in DTYPES.values():
+            outs = [torch.full((t + 2, h, D), 3.0, dtype=dtype, device="cuda") for _ in range(2)]
+            wq.wq_kv_read(*inner, _i32(starts), _i32(edges), t, k_out=outs[0][1:-1],
+                          v_out=outs[1][1:-1])
+            for out in outs:
+                assert bool((out[0] == 3).all()) and bool((out[-1] == 3).all())
+    for x in k_cache + v_cache:
+        assert not x[0].any() and not x[4].any()
