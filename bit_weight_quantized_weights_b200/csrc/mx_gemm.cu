@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(256) mx_scales_kernel(const ScaleArgs a) {
 // a long K, the 2 or 4 CTAs of a cluster share a tile's K. 8192 x 14336 x 4096 with two
 // planes: 325 us with the scale pass, 5.9 POP/s, the tensor cores busy 81% of the
 // cycles (bare MMAs: 6.7 POP/s at the same power); with one plane 197 us, bound by
-// the operands' way from L2; 33 x 4096 x 4096 7.0 us, bound by latency.
+// the operands' way from L2; 33 x 4096 x 4096 6.8 us, bound by latency.
 // ---------------------------------------------------------------------------
 constexpr int kBM = 128;
 constexpr int kBKBytes = 128;   // bytes of a stage's row: 256 k
@@ -795,7 +795,10 @@ wq_status launch_width(const CUtensorMap& tx, const void* wcodes, void* y, const
   // pass is saved. Two planes, K = 4096, with the pass and without, K not split: 33
   // tokens x 4096 features 9.8 and 9.2 us, 64 9.5 and 9.5, 96 9.6 and 10.5, 64 x 14336
   // 11.7 and 12.6; one plane: 33 x 4096 8.7 and 7.3, 128 8.9 and 8.3, 128 x 14336 10.4
-  // and 11.3. A CTA with few stages may have more rows for the same saving.
+  // and 11.3. A CTA with few stages may have more rows for the same saving: where K is
+  // shared (1 to 200 tokens, 1024 to 4608 features, K to 14336, one and two planes: 193
+  // shapes) the pass takes 1.5 to 1.0 of the direct form's time up to 2300 row-stages
+  // and 1.14 to 0.73 of it beyond; the rule's choice is at most 7% from the faster one.
   if constexpr (BN <= 128) {
     const int64_t tiles = (int64_t)a.mt * ((a.N + BN - 1) / BN);
     const int rows = PL * std::min(a.M, kBM) + BN;
@@ -827,6 +830,10 @@ wq_status launch_gemm(const CUtensorMap& tx, const void* wcodes, void* y, const 
   // cluster barriers, and BN floats a row): 128 wide and 4 CTAs 11.0 us, 64 and 2 13.3.
   // With 128 rows and K = 4096 it does not pay: 9.9 us with 32 wide tiles, 12.5 with
   // 128 and 4; with K = 14336 it does: 23.4 and 15.7.
+  // At most 128 CTAs: 33 clusters of 4 are resident at once, and one more takes a second
+  // wave (36 tiles in clusters of 4 instead of 2, 1 x 4608 x 4096: 5.4 and 8.3 us). Of 2
+  // there are 74; 72 tiles in clusters of 2 are not taken yet (1 x 9216 x 11008: 14.5 us
+  // as it is, 10.3).
   if (tiles(bn) <= sms) {
     auto time = [&](int width, int s) {
       const int64_t stage = PL == 1 ? (width == 32 ? 280 : width == 64 ? 330 : 320)

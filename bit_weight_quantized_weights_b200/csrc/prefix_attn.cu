@@ -470,7 +470,7 @@ __device__ __forceinline__ int own_length(const PrefixArgs& p, int b) {
 // KV head x sequence of the own tokens. Bound by its instructions, about 640 a
 // warp's step of 32 keys, half of them dequantization: 64 sequences x 8 heads x 8
 // rows on 2000 to 2048 own tokens take 43 us (141 MB of cache, issue 51%, HBM 42%).
-// With few keys its latency is what counts: 4 chats on 1021 shared keys 8.6 us with
+// With few keys its latency is what counts: 4 chats on 1021 shared keys 7.8 us with
 // the merge. Launched while the tcgen05 kernel still runs, whose results the merge
 // needs too: every CTA ends by waiting for it. Without that kernel it is the call's
 // first and waits at once (ends_waiting false).
