@@ -476,7 +476,8 @@ wq_status wq_kv_block_values(const uint32_t* codes, int64_t rows, int64_t L, int
  *   starts   int32 [B] (device): token t of sequence b is at cache position
  *            starts[b] + t - offsets[b].
  * wq_kv_append quantizes every row as wq_quantize_pack(WQ_FMT_INT4_ASYM, group
- * = D) does its fp32 value, bit for bit, and writes codes, scale and zero.
+ * = D) does its fp32 value, bit for bit, and writes codes, scale and zero (a
+ * range beyond 15 times fp16's largest number: scale infinite, the rest 0).
  * Positions outside 0 .. cap - 1 are not written; all other rows of the cache
  * stay as they were, also those that share a word of V codes with a new one.
  * wq_kv_read writes RN_dtype((q - z) s) of every row (the product is exact in
@@ -521,7 +522,9 @@ wq_status wq_kv_read(const void* k_codes, const void* k_scales, const void* k_ze
  * Tokens behind P and behind a sequence's length are not read, whatever the
  * buffers hold there. The codes enter fp16 tensor-core products as exact
  * integers, except those of the prefix for bf16 queries where the batch is
- * large: there the dequantized values (q - z) s are rounded to fp16. Scores,
+ * large: there the dequantized values (q - z) s are rounded to fp16. (For fp16
+ * queries they enter as (q - z) times the leading 7 bits of s, exactly, and the
+ * rest of s, below 2^-6 of it, is applied rounded to bf16.) Scores,
  * softmax statistics and sums are fp32; the softmax weights are rounded to
  * fp16. Scales are those a quantizer writes (positive and finite); scores are
  * below 2^99 in magnitude. The result of a sequence does not depend on the
