@@ -15,10 +15,10 @@
 //   out_d = sum_j 2^(m_j - M) O_jd / sum_j 2^(m_j - M) E_j over the ranges j.
 // The integers q - z are exact in fp16 and enter the MMAs as they are; the
 // key's scale multiplies the fp32 score, the value's scale goes into the
-// exponent, so that the fp16 weight w_l <= 2^8 carries it whatever its
+// exponent, so that the fp16 weight w_l <= 2^15 carries it whatever its
 // magnitude. q is scaled per row by a power of two into fp16's range (exact
 // for elements down to 2^-28 of the row's largest). The only roundings below
-// fp32 are w's (2^-11 of w, where w >= 2^-14 of the largest) and the output's.
+// fp32 are w's (2^-11 of w, where w >= 2^-21 of the largest) and the output's.
 #include <algorithm>
 #include <cmath>
 
@@ -351,7 +351,7 @@ __device__ __forceinline__ void attend(const PrefixArgs& p, const Cache& c, int6
 #pragma unroll
           for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
           // a row moves by its own scores only, whatever rows share its tile
-          const float nm = mx > m[nt][x] + kSlack ? mx : m[nt][x];
+          const float nm = mx > m[nt][x] + kSlack ? mx - kLift : m[nt][x];
           const float f = ex2(m[nt][x] - nm);
           m[nt][x] = nm;
           E[nt][x] *= f;

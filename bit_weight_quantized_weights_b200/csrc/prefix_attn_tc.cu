@@ -31,7 +31,7 @@
 // and its exponentials 2050 each, its 11200 warp instructions 2800 (softmax 5600,
 // dequantization 3100); a stream's scores, softmax and values follow one another and
 // two streams cover each other in part. 1024 rows x 8 heads x 65537 keys, with the
-// own tokens and the merge: 306 us with bf16 queries (898 TFLOP/s), 392 with fp16;
+// own tokens and the merge: 306 us with bf16 queries (898 TFLOP/s), 388 with fp16;
 // 512 x 8 x 32768: 98 and 118 us.
 //
 // MMAs of one issuing thread execute in order, so S of a tile completes after
@@ -60,7 +60,10 @@ constexpr int kThreads = 28 * 32;
 constexpr int kRegsDequant = 88, kRegsIssue = 40;
 constexpr int kOpBytes = kTile * kD * 2;   // an operand tile: two 64-element atoms of 16 KB
 constexpr int kAtomBytes = kOpBytes / 2;
-constexpr float kSumMax = 2048.0f;         // of a lane's 4 weights, before a bound moves
+// A row's bound is put 2^6 below its largest weight, and moves before a lane's sum of 4
+// weights passes 2^15 (with the scales' rest, at most 2^-4 of it, still in fp16): keys of
+// 2^-19 of the largest weight keep all bits of theirs.
+constexpr float kLiftTc = 6.0f, kSumMax = 32768.0f;
 constexpr int kTabs = 4;                   // key-table stages
 constexpr int kColO = 256;                 // TMEM columns of the outputs (scores: 0 and 128)
 
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         weigh();
-        // No weight is above a lane's sums of 4: while those stay below 2^11 they
+        // No weight is above a lane's sums of 4: while those stay below 2^15 they
         // all fit fp16, and no maximum is needed. The first columns set the
         // bound, whatever their scores.
         const bool first = i == 0 && c == 0;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // a row moves by its own scores only; t is relative to the old bound.
             // Bounds are integers: 2^-up is exact, and so are the products with it
-            const float up = first || sum > kSumMax ? rintf(mx) : 0.0f;
+            const float up = first || sum > kSumMax ? rintf(mx) - kLiftTc : 0.0f;
             f[n] = first ? 1.0f : up < 126.0f ? pow2(-(int)up) : 0.0f;
             m[n] += up;
             E[n] *= f[n];

@@ -148,3 +148,60 @@ def test_operands_are_exact(wq, on, where, path, dtype, spread):
     assert error <= 1.05 ** 2 * limit, (error / limit) ** 0.5
     # the bound tells: the oracle with rounded operands (and exact weights) is beyond it
     assert rounded > 1.05 ** 2 * limit, (rounded / limit) ** 0.5
+
+
+@pytest.mark.parametrize("where,path", [("prefix", 1), ("prefix", 2), ("own", 1)])
+def test_many_keys_far_below_one_keep_their_precision(wq, on, where, path):
+    """One key (the first) about 2^18 above 20000 others, of value 0, as a key that only
+    collects weight: the output is the others' 7%, and their weights, 2^-18 of the largest,
+    are rounded as finely as any (the bound of test_operands_are_exact)."""
+    on(path)
+    b, hq, hkv, n = 2, 8, 1, 20000
+    g = torch.Generator().manual_seed(78)
+    parts = 1 if where == "prefix" else b
+    k = torch.randn(parts, hkv, n, D, generator=g) * 0.1
+    v = torch.randn(parts, hkv, n, D, generator=g)
+    k[:, :, 0] = 18.0 / (1.4426950408889634 * np.sqrt(D))    # of q = 1: 18 steps of the exponent
+    v[:, :, 0] = 0.0
+    q = (1.0 + 0.05 * torch.randn(b, hq, D, generator=g)).half().cuda()
+    cache = wq.kv_quantize_keys(k.cuda()), wq.kv_quantize_values(v.cuda())
+    if where == "prefix":
+        none = torch.zeros(b, dtype=torch.int32, device="cuda")
+        got = wq.wq_prefix_attention(q, *cache, *wq.kv_cache_alloc(b, hkv, 1), none)
+    else:
+        got = wq.wq_prefix_attention(q, None, None, *cache,
+                                     torch.full((b,), n, dtype=torch.int32, device="cuda"))
+    got, qn = got.double().cpu().numpy(), q.double().cpu().numpy()
+    kk, vv = _rows(cache[0], False)[0], _rows(cache[1], True)[0]
+    error = limit = 0.0
+    for i in range(b):
+        _, p, want = _attend(qn[i], kk[i % parts, 0], vv[i % parts, 0])
+        assert p[:, 0].min() > 0.8
+        step = 2.0 ** np.maximum(np.floor(np.log2(np.abs(want))) - 10, -24)
+        error += ((got[i] - want) ** 2).sum()
+        limit += (step ** 2 / 12).sum() + 2.0 ** -20 / 12 * (p ** 2 @ vv[i % parts, 0] ** 2).sum()
+    assert error <= 1.05 ** 2 * limit, (error / limit) ** 0.5
+
+
+def test_many_own_keys_far_below_one_in_a_full_batch(wq):
+    """The same where every sequence and head has one range of keys: 2000 keys a head."""
+    b, hq, hkv, n = 160, 8, 8, 2000
+    g = torch.Generator().manual_seed(79)
+    k = torch.randn(1, hkv, n, D, generator=g) * 0.1
+    v = torch.randn(1, hkv, n, D, generator=g)
+    k[:, :, 0] = 18.0 / (1.4426950408889634 * np.sqrt(D))
+    v[:, :, 0] = 0.0
+    q = (1.0 + 0.05 * torch.randn(b, hq, D, generator=g)).half().cuda()
+    cache = wq.kv_quantize_keys(k.cuda()), wq.kv_quantize_values(v.cuda())
+    full = [tuple(t.repeat(b, *[1] * (t.dim() - 1)) for t in part) for part in cache]
+    got = wq.wq_prefix_attention(q, None, None, *full,
+                                 torch.full((b,), n, dtype=torch.int32, device="cuda"))
+    got, qn = got.double().cpu().numpy(), q.double().cpu().numpy()
+    kk, vv = _rows(cache[0], False)[0], _rows(cache[1], True)[0]
+    error = limit = 0.0
+    for h in range(hkv):
+        _, p, want = _attend(qn[:, h], kk[0, h], vv[0, h])
+        step = 2.0 ** np.maximum(np.floor(np.log2(np.abs(want))) - 10, -24)
+        error += ((got[:, h] - want) ** 2).sum()
+        limit += (step ** 2 / 12).sum() + 2.0 ** -20 / 12 * (p ** 2 @ vv[0, h] ** 2).sum()
+    assert error <= 1.05 ** 2 * limit, (error / limit) ** 0.5
