@@ -145,23 +145,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _scratch(stream, alloc, *args, **kwargs):
-    """Memory for a call on `stream` (None: the current one), from that stream's pool:
-    memory of another pool may still be in use on the stream it belongs to, and what
-    the wrapper drops would go back there while the call runs."""
-    if stream is None:
-        return alloc(*args, **kwargs)
+def _on(stream, wrapper, *args):
+    """A call that is given a stream: made with it as the current one, so that what the
+    wrapper allocates comes from that stream's pool. Memory of another pool may still
+    be in use on the stream it belongs to, and a workspace that the wrapper drops would
+    go back there while the call runs. The results are marked as used on the caller's
+    current stream too."""
     with torch.cuda.stream(stream):
-        return alloc(*args, **kwargs)
-
-
-def _result(stream, alloc, *args, **kwargs):
-    """The same for what the caller gets, who will use it on the current stream too."""
-    out = _scratch(stream, alloc, *args, **kwargs)
-    if stream is not None:
-        for t in out if isinstance(out, tuple) else (out,):
-            if t is not None:
-                t.record_stream(torch.cuda.current_stream(t.device))
+        out = wrapper(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream(t.device))
     return out
 
 
@@ -230,86 +224,100 @@ def alloc_packed(fmt, n, k, group, device="cuda"):
 
 def wq_quantize_pack(fmt, w, group, qweight=None, scales=None, zeros=None, stream=None):
     """Quantize fp32 W [N, K] on the GPU; returns (qweight, scales, zeros)."""
+    if stream is not None:
+        return _on(stream, wq_quantize_pack, fmt, w, group, qweight, scales, zeros)
     _cuda(w, torch.float32, "W")
     n, k = w.shape
     if qweight is None:
-        qweight, scales, zeros = _result(stream, alloc_packed, fmt, n, k, group, w.device)
+        qweight, scales, zeros = alloc_packed(fmt, n, k, group, w.device)
     _check(lib.wq_quantize_pack(fmt, _ptr(w), n, k, group, _ptr(qweight), _ptr(scales),
-                                _ptr(zeros), _stream(stream)), "wq_quantize_pack")
+                                _ptr(zeros), _stream()), "wq_quantize_pack")
     return qweight, scales, zeros
 
 
 def wq_unpack(fmt, qweight, n, k, out=None, stream=None):
+    if stream is not None:
+        return _on(stream, wq_unpack, fmt, qweight, n, k, out)
     _cuda(qweight, None, "qweight")
     if out is None:
-        out = _result(stream, torch.empty, n * k, dtype=torch.uint8, device=qweight.device)
-    _check(lib.wq_unpack(fmt, _ptr(qweight), n, k, _ptr(out), _stream(stream)), "wq_unpack")
+        out = torch.empty(n * k, dtype=torch.uint8, device=qweight.device)
+    _check(lib.wq_unpack(fmt, _ptr(qweight), n, k, _ptr(out), _stream()), "wq_unpack")
     return out
 
 
 def wq_nf4_dequant(codes, absmax, numel, out=None, out_dtype=torch.bfloat16, stream=None):
+    if stream is not None:
+        return _on(stream, wq_nf4_dequant, codes, absmax, numel, out, out_dtype)
     _cuda(codes, torch.uint8, "codes")
     _cuda(absmax, torch.float32, "absmax")
     if out is None:
-        out = _result(stream, torch.empty, numel, dtype=out_dtype, device=codes.device)
+        out = torch.empty(numel, dtype=out_dtype, device=codes.device)
     dt = WQ_BF16 if out.dtype == torch.bfloat16 else WQ_FP16
     _check(lib.wq_nf4_dequant(_ptr(codes), _ptr(absmax), numel, 64, _ptr(out), dt,
-                              _stream(stream)), "wq_nf4_dequant")
+                              _stream()), "wq_nf4_dequant")
     return out
 
 
 def wq_int4_dequant(qweight, scales, zeros, n, k, group, out=None, out_dtype=torch.bfloat16,
                     stream=None):
+    if stream is not None:
+        return _on(stream, wq_int4_dequant, qweight, scales, zeros, n, k, group, out, out_dtype)
     _cuda(qweight, torch.int32, "qweight")
     _cuda(scales, torch.float16, "scales")
     _cuda(zeros, torch.float16, "zeros")
     if out is None:
-        out = _result(stream, torch.empty, n, k, dtype=out_dtype, device=qweight.device)
+        out = torch.empty(n, k, dtype=out_dtype, device=qweight.device)
     dt = WQ_BF16 if out.dtype == torch.bfloat16 else WQ_FP16
     _check(lib.wq_int4_dequant(_ptr(qweight), _ptr(scales), _ptr(zeros), n, k, group, _ptr(out),
-                               dt, _stream(stream)), "wq_int4_dequant")
+                               dt, _stream()), "wq_int4_dequant")
     return out
 
 
-def _product(fn, name, x, n, fmt, group, qweight, scales, zeros, out, workspace, stream):
+def _product(fn, name, x, n, fmt, group, qweight, scales, zeros, out, workspace):
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _cuda(out, torch.bfloat16, "y")
     ws = _ptr(workspace)
     wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(fn(_ptr(x), m, n, k, fmt, group, _ptr(qweight), _ptr(scales), _ptr(zeros), _ptr(out),
-              ws, wsb, _stream(stream)), name)
+              ws, wsb, _stream()), name)
     return out
 
 
 def wq_w4a16_gemv(x, n, fmt, group, qweight, scales, zeros, out=None, stream=None):
     """Decode GEMV: x bf16 [M<=16, K] -> y bf16 [M, N]."""
+    if stream is not None:
+        return _on(stream, wq_w4a16_gemv, x, n, fmt, group, qweight, scales, zeros, out)
     return _product(lib.wq_w4a16_gemv, "wq_w4a16_gemv", x, n, fmt, group, qweight, scales, zeros,
-                    out, None, stream)
+                    out, None)
 
 
 def wq_residual(fmt, w, group, qweight, scales, zeros, out=None, stream=None):
     """R^T = fp16(W - dequant(W_q)) as fp16 [K, N] from fp32 W [N, K]."""
+    if stream is not None:
+        return _on(stream, wq_residual, fmt, w, group, qweight, scales, zeros, out)
     _cuda(w, torch.float32, "W")
     n, k = w.shape
     if out is None:
-        out = _result(stream, torch.empty, k, n, dtype=torch.float16, device=w.device)
+        out = torch.empty(k, n, dtype=torch.float16, device=w.device)
     _cuda(out, torch.float16, "residual_t")
     _check(lib.wq_residual(fmt, _ptr(w), n, k, group, _ptr(qweight), _ptr(scales), _ptr(zeros),
-                           _ptr(out), _stream(stream)), "wq_residual")
+                           _ptr(out), _stream()), "wq_residual")
     return out
 
 
 def wq_select_salient(x, k, out=None, stream=None):
     """The k salient channels of bf16 x [M, K] as int32 [k], increasing."""
+    if stream is not None:
+        return _on(stream, wq_select_salient, x, k, out)
     _cuda(x, torch.bfloat16, "x")
     m, kk = x.shape
     if out is None:
-        out = _result(stream, torch.empty, max(k, 0), dtype=torch.int32, device=x.device)
+        out = torch.empty(max(k, 0), dtype=torch.int32, device=x.device)
     _cuda(out, torch.int32, "idx")
-    _check(lib.wq_select_salient(_ptr(x), m, kk, k, _ptr(out), _stream(stream)),
+    _check(lib.wq_select_salient(_ptr(x), m, kk, k, _ptr(out), _stream()),
            "wq_select_salient")
     return out
 
@@ -317,15 +325,18 @@ def wq_select_salient(x, k, out=None, stream=None):
 def wq_w4a16_gemv_corrected(x, n, fmt, group, qweight, scales, zeros, residual_t, idx, out=None,
                             stream=None):
     """Decode GEMV plus the residuals of the channels idx (int32 [k])."""
+    if stream is not None:
+        return _on(stream, wq_w4a16_gemv_corrected, x, n, fmt, group, qweight, scales, zeros,
+                   residual_t, idx, out)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _cuda(out, torch.bfloat16, "y")
     nsel = 0 if idx is None else idx.numel()
     _check(lib.wq_w4a16_gemv_corrected(_ptr(x), m, n, k, fmt, group, _ptr(qweight), _ptr(scales),
                                        _ptr(zeros), _ptr(residual_t), _ptr(idx), nsel, _ptr(out),
-                                       _stream(stream)), "wq_w4a16_gemv_corrected")
+                                       _stream()), "wq_w4a16_gemv_corrected")
     return out
 
 
@@ -334,17 +345,20 @@ def wq_w4a16_gemv_salient(x, n, fmt, group, qweight, scales, zeros, residual_t, 
     """One corrected decode step: select the nsel salient channels into idx
     (int32 scratch, allocated if None), then the corrected GEMV, launched to
     overlap the selection. Returns y."""
+    if stream is not None:
+        return _on(stream, wq_w4a16_gemv_salient, x, n, fmt, group, qweight, scales, zeros,
+                   residual_t, nsel, idx, out)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _cuda(out, torch.bfloat16, "y")
     if idx is None:
-        idx = _scratch(stream, torch.empty, max(nsel, 1), dtype=torch.int32, device=x.device)
+        idx = torch.empty(max(nsel, 1), dtype=torch.int32, device=x.device)
     _cuda(idx, torch.int32, "idx")
     _check(lib.wq_w4a16_gemv_salient(_ptr(x), m, n, k, fmt, group, _ptr(qweight), _ptr(scales),
                                      _ptr(zeros), _ptr(residual_t), nsel, _ptr(idx), _ptr(out),
-                                     _stream(stream)), "wq_w4a16_gemv_salient")
+                                     _stream()), "wq_w4a16_gemv_salient")
     return out
 
 
@@ -356,23 +370,26 @@ def gemm_workspace(m, n, k, group, device="cuda"):
 def wq_w4a16_gemm(x, n, fmt, group, qweight, scales, zeros, workspace=None, out=None,
                   stream=None):
     """Prefill GEMM with fused dequantization on tcgen05: y bf16 [M, N]."""
+    if stream is not None:
+        return _on(stream, wq_w4a16_gemm, x, n, fmt, group, qweight, scales, zeros, workspace, out)
     _cuda(x, torch.bfloat16, "x")
     if workspace is None:
-        workspace = _scratch(stream, gemm_workspace, x.shape[0], n, x.shape[1], group, x.device)
+        workspace = gemm_workspace(x.shape[0], n, x.shape[1], group, x.device)
     return _product(lib.wq_w4a16_gemm, "wq_w4a16_gemm", x, n, fmt, group, qweight, scales, zeros,
-                    out, workspace, stream)
+                    out, workspace)
 
 
 def wq_msd_decompose(x, n_components=2, digits=None, comp_scales=None, stream=None):
     """Digit planes int8 [C, M, K] and scales fp32 [C, M] of bf16 x [M, K]."""
+    if stream is not None:
+        return _on(stream, wq_msd_decompose, x, n_components, digits, comp_scales)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if digits is None:
-        digits = _result(stream, torch.empty, n_components, m, k, dtype=torch.int8, device=x.device)
-        comp_scales = _result(stream, torch.empty, n_components, m, dtype=torch.float32,
-                              device=x.device)
+        digits = torch.empty(n_components, m, k, dtype=torch.int8, device=x.device)
+        comp_scales = torch.empty(n_components, m, dtype=torch.float32, device=x.device)
     _check(lib.wq_msd_decompose(_ptr(x), m, k, n_components, _ptr(digits), _ptr(comp_scales),
-                                _stream(stream)), "wq_msd_decompose")
+                                _stream()), "wq_msd_decompose")
     return digits, comp_scales
 
 
@@ -384,15 +401,18 @@ def msd_workspace(m, n, k, group, n_components=2, device="cuda"):
 def wq_msd_gemm(x, n, n_components, group, qweight, scales, zeros, workspace=None, out=None,
                 stream=None):
     """Multi-Scale Dequant GEMM: y bf16 [M, N] from int8 digit planes of x."""
+    if stream is not None:
+        return _on(stream, wq_msd_gemm, x, n, n_components, group, qweight, scales, zeros,
+                   workspace, out)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if workspace is None:
-        workspace = _scratch(stream, msd_workspace, m, n, k, group, n_components, x.device)
+        workspace = msd_workspace(m, n, k, group, n_components, x.device)
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_msd_gemm(_ptr(x), m, n, k, n_components, group, _ptr(qweight), _ptr(scales),
                            _ptr(zeros), _ptr(out), _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), _stream(stream)),
+                           workspace.numel() * workspace.element_size(), _stream()),
            "wq_msd_gemm")
     return out
 
@@ -402,12 +422,15 @@ def wq_msd_gemm_noalloc(x, n, n_components, group, qweight, scales, zeros, out=N
     """wq_msd_gemm without a workspace: the library's fixed device scratch array
     is used, so the call allocates nothing (problem size limited to 8 MiB of
     scratch; calls overlapping on the GPU race on it)."""
+    if stream is not None:
+        return _on(stream, wq_msd_gemm_noalloc, x, n, n_components, group, qweight, scales, zeros,
+                   out)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_msd_gemm_noalloc(_ptr(x), m, n, k, n_components, group, _ptr(qweight),
-                                   _ptr(scales), _ptr(zeros), _ptr(out), _stream(stream)),
+                                   _ptr(scales), _ptr(zeros), _ptr(out), _stream()),
            "wq_msd_gemm_noalloc")
     return out
 
@@ -428,28 +451,31 @@ def wq_test_set_wait(limit_ns=0, stall=0):
 
 def wq_mx_quantize(w, codes=None, scales=None, stream=None):
     """MXFP4 weights: w fp32 [N, K] -> (codes uint8 [N, K/2], scale bytes uint8 [N, K/32])."""
+    if stream is not None:
+        return _on(stream, wq_mx_quantize, w, codes, scales)
     _cuda(w, torch.float32, "w")
     n, k = w.shape
     if codes is None:
-        codes = _result(stream, torch.empty, n, k // 2, dtype=torch.uint8, device=w.device)
+        codes = torch.empty(n, k // 2, dtype=torch.uint8, device=w.device)
     if scales is None:
-        scales = _result(stream, torch.empty, n, k // 32, dtype=torch.uint8, device=w.device)
-    _check(lib.wq_mx_quantize(_ptr(w), n, k, _ptr(codes), _ptr(scales), _stream(stream)),
+        scales = torch.empty(n, k // 32, dtype=torch.uint8, device=w.device)
+    _check(lib.wq_mx_quantize(_ptr(w), n, k, _ptr(codes), _ptr(scales), _stream()),
            "wq_mx_quantize")
     return codes, scales
 
 
 def wq_mx_decompose(x, n_passes=2, planes=None, scales=None, stream=None):
     """x bf16 [M, K] -> (planes uint8 [P, M, K] E4M3 bytes, scale bytes uint8 [P, M, K/32])."""
+    if stream is not None:
+        return _on(stream, wq_mx_decompose, x, n_passes, planes, scales)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if planes is None:
-        planes = _result(stream, torch.empty, n_passes, m, k, dtype=torch.uint8, device=x.device)
+        planes = torch.empty(n_passes, m, k, dtype=torch.uint8, device=x.device)
     if scales is None:
-        scales = _result(stream, torch.empty, n_passes, m, k // 32, dtype=torch.uint8,
-                         device=x.device)
+        scales = torch.empty(n_passes, m, k // 32, dtype=torch.uint8, device=x.device)
     _check(lib.wq_mx_decompose(_ptr(x), m, k, n_passes, _ptr(planes), _ptr(scales),
-                               _stream(stream)), "wq_mx_decompose")
+                               _stream()), "wq_mx_decompose")
     return planes, scales
 
 
@@ -460,20 +486,24 @@ def mx_workspace(m, n, k, n_passes=2, device="cuda"):
 
 def wq_mx_gemv(x, n, n_passes, codes, scales, workspace=None, out=None, stream=None):
     """y bf16 [M, N] = x_hat . w_hat^T (MXFP4 weights; two MXFP4 passes or one MXFP8 pass)."""
+    if stream is not None:
+        return _on(stream, wq_mx_gemv, x, n, n_passes, codes, scales, workspace, out)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if workspace is None:
-        workspace = _scratch(stream, mx_workspace, m, n, k, n_passes, x.device)
+        workspace = mx_workspace(m, n, k, n_passes, x.device)
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_mx_gemv(_ptr(x), m, n, k, n_passes, _ptr(codes), _ptr(scales), _ptr(out),
-                          _ptr(workspace), workspace.numel(), _stream(stream)), "wq_mx_gemv")
+                          _ptr(workspace), workspace.numel(), _stream()), "wq_mx_gemv")
     return out
 
 
 def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     """MXFP4 activations kept in 4 bits: x [M, K] (bf16, fp16 or fp32; rows may
     be strided) -> (planes uint8 [P, M, K/2], scale bytes uint8 [P, M, K/32])."""
+    if stream is not None:
+        return _on(stream, wq_mx_quantize_planes, x, n_planes, planes, scales)
     dev = _current_device()
     dt = _DTYPES.get(x.dtype)
     if dt is None or x.dim() != 2:
@@ -483,12 +513,12 @@ def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
     if inner != 1 and k > 1:
         raise ValueError("the rows of x must be contiguous")
     if planes is None:
-        planes = _result(stream, x.new_empty, (n_planes, m, k // 2), dtype=torch.uint8)
+        planes = x.new_empty((n_planes, m, k // 2), dtype=torch.uint8)
     elif planes.dtype is not torch.uint8 or planes.shape != (n_planes, m, k // 2) or \
             not planes.is_contiguous():
         raise ValueError("planes must be uint8 [%d, %d, %d]" % (n_planes, m, k // 2))
     if scales is None:
-        scales = _result(stream, planes.new_empty, (n_planes, m, k // 32))
+        scales = planes.new_empty((n_planes, m, k // 32))
     elif scales.dtype is not torch.uint8 or scales.shape != (n_planes, m, k // 32) or \
             not scales.is_contiguous():
         raise ValueError("scales must be uint8 [%d, %d, %d]" % (n_planes, m, k // 32))
@@ -496,7 +526,7 @@ def wq_mx_quantize_planes(x, n_planes=2, planes=None, scales=None, stream=None):
         _on_device(dev, x, planes, scales)
     status = lib.wq_mx_quantize_planes(
         x.data_ptr(), dt, ldx if m > 1 else k, m, k, n_planes, planes.data_ptr(),
-        scales.data_ptr(), _raw_stream(dev) if stream is None else stream.cuda_stream)
+        scales.data_ptr(), _raw_stream(dev))
     if status:
         raise WqError(status, "wq_mx_quantize_planes")
     return planes, scales
@@ -511,6 +541,8 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
     """y bf16 [M, N] = (sum of the MXFP4 planes) . w_hat^T for any M, on the FP4
     tensor cores: planes and plane_scales as wq_mx_quantize_planes returns
     them, codes and scales as wq_mx_quantize packs the weights [N, K]."""
+    if stream is not None:
+        return _on(stream, wq_mx_gemm, planes, plane_scales, n, codes, scales, workspace, out)
     dev = _current_device()
     if planes.dtype is not _U8 or plane_scales.dtype is not _U8 or codes.dtype is not _U8 or \
             scales.dtype is not _U8 or not planes.is_contiguous() or \
@@ -526,9 +558,9 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
         raise ValueError("scales or weights do not match planes %s and N = %d"
                          % (tuple(planes.shape), n))
     if workspace is None:
-        workspace = _scratch(stream, mx_gemm_workspace, m, n, k, p, planes.device)
+        workspace = mx_gemm_workspace(m, n, k, p, planes.device)
     if out is None:
-        out = _result(stream, planes.new_empty, (m, n), dtype=torch.bfloat16)
+        out = planes.new_empty((m, n), dtype=torch.bfloat16)
     elif out.dtype is not torch.bfloat16 or out.shape != (m, n) or not out.is_contiguous():
         raise ValueError("y must be bfloat16 [%d, %d], contiguous" % (m, n))
     if planes.get_device() != dev or plane_scales.get_device() != dev or \
@@ -538,7 +570,7 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
     status = lib.wq_mx_gemm(
         planes.data_ptr(), plane_scales.data_ptr(), m, n, k, p, codes.data_ptr(),
         scales.data_ptr(), out.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+        workspace.nbytes, _raw_stream(dev))
     if status:
         raise WqError(status, "wq_mx_gemm")
     return out
@@ -546,14 +578,16 @@ def wq_mx_gemm(planes, plane_scales, n, codes, scales, workspace=None, out=None,
 
 def wq_msd_gemm_nf4(x, n, n_components, codes, absmax, workspace=None, out=None, stream=None):
     """Decode MSD product with NF4 weights (integer codebook digits); M <= 16."""
+    if stream is not None:
+        return _on(stream, wq_msd_gemm_nf4, x, n, n_components, codes, absmax, workspace, out)
     _cuda(x, torch.bfloat16, "x")
     m, k = x.shape
     if workspace is None:
-        workspace = _scratch(stream, msd_workspace, m, n, k, 64, n_components, x.device)
+        workspace = msd_workspace(m, n, k, 64, n_components, x.device)
     if out is None:
-        out = _result(stream, torch.empty, m, n, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(m, n, dtype=torch.bfloat16, device=x.device)
     _check(lib.wq_msd_gemm_nf4(_ptr(x), m, n, k, n_components, _ptr(codes), _ptr(absmax),
-                               _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
+                               _ptr(out), _ptr(workspace), workspace.numel(), _stream()),
            "wq_msd_gemm_nf4")
     return out
 
@@ -562,20 +596,24 @@ def kv_quantize_keys(k, stream=None):
     """INT4-quantize a key cache fp32 [B, Hkv, L, D] on the GPU, one group per
     (sequence, head, token) row: returns (codes int32 [B, Hkv, L, D/8], scales
     fp16 [B, Hkv, L], zeros fp16 [B, Hkv, L])."""
+    if stream is not None:
+        return _on(stream, kv_quantize_keys, k)
     _cuda(k, torch.float32, "k")
     b, hkv, length, d = k.shape
-    qw, sc, zr = wq_quantize_pack(WQ_FMT_INT4_ASYM, k.reshape(-1, d), d, stream=stream)
+    qw, sc, zr = wq_quantize_pack(WQ_FMT_INT4_ASYM, k.reshape(-1, d), d)
     return (qw.view(b, hkv, length, d // 8), sc.view(b, hkv, length), zr.view(b, hkv, length))
 
 
 def wq_kv_block_values(codes, rows, length, d, out=None, stream=None):
     """V codes from the token layout (int32 [rows * L, D/8]) to blocks of 8
     tokens: int32 [rows, ceil(L/8), D]."""
+    if stream is not None:
+        return _on(stream, wq_kv_block_values, codes, rows, length, d, out)
     _cuda(codes, torch.int32, "codes")
     nblk = (length + 7) // 8
     if out is None:
-        out = _result(stream, torch.empty, rows, nblk, d, dtype=torch.int32, device=codes.device)
-    _check(lib.wq_kv_block_values(_ptr(codes), rows, length, d, _ptr(out), _stream(stream)),
+        out = torch.empty(rows, nblk, d, dtype=torch.int32, device=codes.device)
+    _check(lib.wq_kv_block_values(_ptr(codes), rows, length, d, _ptr(out), _stream()),
            "wq_kv_block_values")
     return out
 
@@ -584,10 +622,12 @@ def kv_quantize_values(v, stream=None):
     """INT4-quantize a value cache fp32 [B, Hkv, L, D] on the GPU, one group per
     (sequence, head, token) row: returns (codes int32 [B, Hkv, ceil(L/8), D] in
     blocks of 8 tokens, scales fp16 [B, Hkv, L], zeros fp16 [B, Hkv, L])."""
+    if stream is not None:
+        return _on(stream, kv_quantize_values, v)
     _cuda(v, torch.float32, "v")
     b, hkv, length, d = v.shape
-    qw, sc, zr = wq_quantize_pack(WQ_FMT_INT4_ASYM, v.reshape(-1, d), d, stream=stream)
-    blocked = wq_kv_block_values(qw, b * hkv, length, d, stream=stream)
+    qw, sc, zr = wq_quantize_pack(WQ_FMT_INT4_ASYM, v.reshape(-1, d), d)
+    blocked = wq_kv_block_values(qw, b * hkv, length, d)
     return (blocked.view(b, hkv, (length + 7) // 8, d), sc.view(b, hkv, length),
             zr.view(b, hkv, length))
 
@@ -674,6 +714,8 @@ def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
     16-byte aligned), sequence b's being offsets[b] .. offsets[b + 1] - 1
     (int32 [B + 1]), written from cache position starts[b] (int32 [B]) on.
     k_cache and v_cache (kv_cache_alloc) are updated in place."""
+    if stream is not None:
+        return _on(stream, wq_kv_append, k, v, k_cache, v_cache, starts, offsets)
     dev = _current_device()
     b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     t, dt, ks, vs = _kv_rows(k, v, cache, starts, offsets, dev)
@@ -683,7 +725,7 @@ def wq_kv_append(k, v, k_cache, v_cache, starts, offsets, stream=None):
         k.data_ptr(), v.data_ptr(), dt, t, hkv, d, ks, vs, b, starts.data_ptr(),
         offsets.data_ptr(), cap, kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(),
         vq.data_ptr(), vscale.data_ptr(), vzero.data_ptr(),
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        _raw_stream(dev))
     if status:
         raise WqError(status, "wq_kv_append")
 
@@ -695,13 +737,16 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
     b (offsets[b] <= t < offsets[b + 1]) from cache position starts[b] + t -
     offsets[b]. Rows behind offsets[B] of a given k_out and v_out stay as they
     were."""
+    if stream is not None:
+        return _on(stream, wq_kv_read, k_cache, v_cache, starts, offsets, total, dtype, k_out,
+                   v_out)
     dev = _current_device()
     b, hkv, cap, d = cache = _kv_cache(k_cache, v_cache, dev)
     if k_out is None:
-        k_out = _result(stream, k_cache[1].new_empty, (total, hkv, d), dtype=dtype)
+        k_out = k_cache[1].new_empty((total, hkv, d), dtype=dtype)
     if v_out is None:
-        v_out = _result(stream, torch.empty_like, k_out) if k_out.is_contiguous() else \
-            _result(stream, k_out.new_empty, (total, hkv, d))
+        v_out = torch.empty_like(k_out) if k_out.is_contiguous() else \
+            k_out.new_empty((total, hkv, d))
     t, dt, ks, vs = _kv_rows(k_out, v_out, cache, starts, offsets, dev)
     if t != total:
         raise ValueError("k_out and v_out must have %d rows" % total)
@@ -711,7 +756,7 @@ def wq_kv_read(k_cache, v_cache, starts, offsets, total, dtype=torch.bfloat16, k
         kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(), vscale.data_ptr(),
         vzero.data_ptr(), b, hkv, d, cap, starts.data_ptr(), offsets.data_ptr(), t,
         k_out.data_ptr(), v_out.data_ptr(), dt, ks, vs,
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        _raw_stream(dev))
     if status:
         raise WqError(status, "wq_kv_read")
     return k_out, v_out
@@ -734,6 +779,9 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
     k_cache and v_cache a cache of B sequences, of which sequence b attends the
     first lengths[b] (int32 [B]) tokens. Returns out [B, Hq, D] of q's type.
     prefix_k = prefix_v = None: no prefix."""
+    if stream is not None:
+        return _on(stream, wq_prefix_attention, q, prefix_k, prefix_v, k_cache, v_cache, lengths,
+                   prefix_len, workspace, out)
     dev = _current_device()
     b, hkv, cap, d = _kv_cache(k_cache, v_cache, dev)
     shape, kind = q.shape, q.dtype
@@ -763,11 +811,9 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
         pre = (kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(),
                vscale.data_ptr(), vzero.data_ptr())
     if workspace is None:
-        workspace = _scratch(stream, prefix_attention_workspace, b, hq, hkv, prefix_len, cap, d,
-                             q.device)
+        workspace = prefix_attention_workspace(b, hq, hkv, prefix_len, cap, d, q.device)
     if out is None:
-        out = _result(stream, torch.empty_like, q) if q.is_contiguous() else \
-            _result(stream, q.new_empty, shape)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
     elif out.dtype is not kind or out.shape != shape or not out.is_contiguous():
         raise ValueError("out must have q's type and shape, contiguous")
     if q.get_device() != dev or lengths.get_device() != dev or \
@@ -780,7 +826,7 @@ def wq_prefix_attention(q, prefix_k, prefix_v, k_cache, v_cache, lengths, prefix
         *pre, cap, kq.data_ptr(), kscale.data_ptr(), kzero.data_ptr(), vq.data_ptr(),
         vscale.data_ptr(), vzero.data_ptr(), lengths.data_ptr(), out.data_ptr(),
         workspace.data_ptr(), workspace.nbytes,
-        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        _raw_stream(dev))
     if status:
         raise WqError(status, "wq_prefix_attention")
     return out
@@ -799,6 +845,9 @@ def wq_msd_decode_attention(q, k_cache, v_cache, n_components=2, workspace=None,
     """MSD decode attention: q bf16 [B, Hq, D]; k_cache and v_cache = (codes,
     scales, zeros) as kv_quantize_keys and kv_quantize_values return them.
     Returns out bf16 [B, Hq, D]."""
+    if stream is not None:
+        return _on(stream, wq_msd_decode_attention, q, k_cache, v_cache, n_components, workspace,
+                   out)
     _cuda(q, torch.bfloat16, "q")
     b, hq, d = q.shape
     kq, ks, kz = k_cache
@@ -814,13 +863,12 @@ def wq_msd_decode_attention(q, k_cache, v_cache, n_components=2, workspace=None,
             tuple(vz.shape) != tuple(ks.shape) or ks.shape[0] != b:
         raise ValueError("KV cache shapes do not match q")
     if workspace is None:
-        workspace = _scratch(stream, attention_workspace, b, hq, hkv, length, d, n_components,
-                             q.device)
+        workspace = attention_workspace(b, hq, hkv, length, d, n_components, q.device)
     if out is None:
-        out = _result(stream, torch.empty, b, hq, d, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(b, hq, d, dtype=torch.bfloat16, device=q.device)
     _check(lib.wq_msd_decode_attention(_ptr(q), b, hq, hkv, length, d, n_components, _ptr(kq),
                                        _ptr(ks), _ptr(kz), _ptr(vq), _ptr(vs), _ptr(vz), _ptr(out),
-                                       _ptr(workspace), workspace.numel(), _stream(stream)),
+                                       _ptr(workspace), workspace.numel(), _stream()),
            "wq_msd_decode_attention")
     return out
 

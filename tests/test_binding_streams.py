@@ -1,5 +1,5 @@
-"""The binding's `stream=` argument, on the host: what a wrapper allocates for a call on a
-given stream comes from that stream's pool."""
+"""The binding on the host: a call with `stream=` is made with that stream current, so that
+what the wrapper allocates comes from that stream's pool; and what needs no GPU."""
 
 import ast
 import contextlib
@@ -29,8 +29,8 @@ class Block:
         self.used_on.append(stream)
 
 
-def test_memory_belongs_to_the_given_stream(wq, monkeypatch):
-    """Allocated with it current; a result is marked as used on the caller's stream."""
+def test_a_call_on_a_stream_is_made_with_it_current(wq, monkeypatch):
+    """What it allocates is that stream's; its results are marked as used on the caller's."""
     current = ["caller"]
 
     @contextlib.contextmanager
@@ -39,38 +39,35 @@ def test_memory_belongs_to_the_given_stream(wq, monkeypatch):
         yield
         current.pop()
 
-    def alloc(n, tuples=False):
+    def wrapper(n, tuples=False):
         blocks = tuple(Block(current[-1]) for _ in range(n))
         return blocks + (None,) if tuples else blocks[0]
 
     monkeypatch.setattr(wq.torch.cuda, "stream", stream)
     monkeypatch.setattr(wq.torch.cuda, "current_stream", lambda device=None: current[-1])
-    for make, used in ((wq._scratch, []), (wq._result, ["caller"])):
-        one = make("side", alloc, 1)
-        assert one.stream == "side" and one.used_on == used
-        for t in make("side", alloc, 3, tuples=True)[:3]:
-            assert t.stream == "side" and t.used_on == used
-        one = make(None, alloc, 1)
-        assert one.stream == "caller" and one.used_on == []
+    results = [wq._on("side", wrapper, 1)] + list(wq._on("side", wrapper, 3, True)[:3])
+    assert all(t.stream == "side" and t.used_on == ["caller"] for t in results)
     assert current == ["caller"]
 
 
-def test_no_wrapper_with_a_stream_allocates_past_it(wq):
-    """Every allocation in a function that takes `stream` goes through the two."""
+def test_every_wrapper_with_a_stream_goes_on_it_first(wq):
+    """Each begins with the same call of itself, with all its other arguments, on the stream."""
     with open(wq.__file__) as f:
         tree = ast.parse(f.read())
     checked = 0
     for fn in tree.body:
-        if not isinstance(fn, ast.FunctionDef) or fn.name in ("_scratch", "_result", "_stream") or \
-                "stream" not in [a.arg for a in fn.args.args]:
+        if not isinstance(fn, ast.FunctionDef):
+            continue
+        names = [a.arg for a in fn.args.args]
+        # (the error word's read allocates nothing)
+        if "stream" not in names or fn.name in ("_on", "_stream", "wq_device_error"):
             continue
         checked += 1
-        for call in ast.walk(fn):
-            if isinstance(call, ast.Call):
-                name = call.func.attr if isinstance(call.func, ast.Attribute) else call.func.id
-                assert not name.startswith(("empty", "zeros", "new_", "alloc_")) and \
-                    not name.endswith("workspace"), (fn.name, name, call.lineno)
-    assert checked >= 25
+        body = fn.body[1:] if ast.get_docstring(fn) is not None else fn.body
+        rest = [n for n in names if n != "stream"]
+        assert ast.unparse(body[0]) == "if stream is not None:\n    return _on(stream, %s)" % \
+            ", ".join([fn.name] + rest), fn.name
+    assert checked == 26
 
 
 def test_host_calls_work_on_a_torch_without_cuda(wq):
